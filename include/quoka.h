@@ -353,6 +353,142 @@ quoka_status sparse_chunk_attn_selcache(const quoka_shape* shape, const void* q_
                                         void* workspace, size_t ws_bytes, void* stream);
 
 /*
+ * window_chunk_attn - attention of the chunk over a sliding window of the cache and a few
+ * first tokens that stay visible: the static counterpart of the selection above, for
+ * layers that attend locally.
+ *
+ * Query t of head h (KV head g = h / G) of sequence b, at position p = P + t with
+ * P = prefix_len[b], attends to the keys
+ *     { j <= p : j < n_sink  or  j > p - window }
+ * of its sequence, out = softmax(q . k^T / sqrt(head_dim)) . v with fp32 accumulation and
+ * softmax, stored in `dtype`.  window >= P + chunk sees every earlier key.  Each query sees
+ * at least its own key.  Rows of the cache that no query sees are not used, and what a key
+ * or value holds reaches only the queries that see it, infinities and NaN included.
+ * chunk = 1 (a decode step) runs the kernel of paged_decode_attn, the keys of each
+ * (sequence, KV head) split over the SMs; longer chunks run per query tile.
+ *
+ *   q_chunk, k_cache, v_cache, kv_off, prefix_len   as for sparse_chunk_attn: the chunk's
+ *               own rows have been written (rows prefix_len[b] .. + chunk - 1)
+ *   window      >= 1: latest keys a query sees, its own included
+ *   n_sink      >= 0: first tokens that every query sees
+ *   out         device [batch, h_q, chunk, head_dim]; must not alias an input
+ *   workspace   device scratch of window_chunk_attn_workspace_size(shape, max_b prefix_len[b],
+ *               window) bytes (may be NULL when that size is 0); contents on entry ignored
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, const void* k_cache,
+                               const void* v_cache, const int64_t* kv_off, const int32_t* prefix_len,
+                               int window, int n_sink, void* out, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* Bytes of device scratch window_chunk_attn() needs (0 unless chunk = 1; 0 if invalid). */
+size_t window_chunk_attn_workspace_size(const quoka_shape* shape, int max_prefix, int window);
+
+/*
+ * A paged KV cache.
+ *
+ * K and V live in pools of pages, k_pages / v_pages [num_pages, h_kv, page_size, head_dim]
+ * (dtype).  Position j of sequence b is slot j % page_size of page
+ * block_table[b * max_pages + j / page_size].  A record of the attention weight that every
+ * key received, record [num_pages, h_kv, page_size] fp32, belongs to the pools when the
+ * cache is to be shrunk by it.  All pools, tables and lengths are the caller's device
+ * memory; lengths and tables are read when the kernels run, so a captured graph can be
+ * replayed while they change.  max_len is the host's bound on the lengths: it sizes the
+ * launch and the workspace.  A length outside [0, max_len] is held to that range, a key
+ * whose page is not in [0, num_pages) is not seen (or not written), and both set bit 2 of
+ * the device error word.
+ */
+#define QUOKA_MAX_PAGED_BATCH 1024  /* sequences per paged call                          */
+#define QUOKA_MAX_PAGE 1024         /* tokens per page                                   */
+
+typedef struct {
+  int batch;          /* sequences, 1..QUOKA_MAX_PAGED_BATCH                           */
+  int h_q;            /* query heads                                                   */
+  int h_kv;           /* KV heads; h_q % h_kv == 0, h_q / h_kv <= QUOKA_MAX_GROUP      */
+  int head_dim;       /* 64 or 128                                                     */
+  quoka_dtype dtype;  /* element type of queries, pools and outputs                    */
+  int page_size;      /* tokens per page: a multiple of 8, 8..QUOKA_MAX_PAGE            */
+  int num_pages;      /* pages in the pools                                            */
+  int max_pages;      /* row length of block_table                                     */
+} quoka_paged_shape;
+
+/*
+ * paged_append - new K/V rows into the pages: row t of sequence b goes to position
+ * start[b] + t, t < n_new (t < count[b] when count is given; the rows after it are not
+ * read).  The record of the rows, when given, is set to 0.  Other rows are untouched.
+ *
+ *   k_new, v_new  device [batch, h_kv, n_new, head_dim]
+ *   n_new       1..QUOKA_MAX_CHUNK
+ *   start       device int32 [batch]: tokens in the cache before the append
+ *   count       device int32 [batch] or NULL: rows of each sequence, 0..n_new
+ *   record      device fp32 pool or NULL
+ * A position at or past max_pages * page_size is not written and sets bit 2 of the device
+ * error word.  Two rows of one call must not fall on one slot.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+quoka_status paged_append(const quoka_paged_shape* shape, const void* k_new, const void* v_new, int n_new,
+                          void* k_pages, void* v_pages, float* record, const int32_t* block_table,
+                          const int32_t* start, const int32_t* count, void* stream);
+
+/*
+ * paged_decode_attn - attention of one new token per sequence over its pages.
+ *
+ * The query of head h (KV head g = h / G) of sequence b, n = seq_len[b], attends to the
+ * keys { j < n : j < n_sink or j >= n - window } (the new token's own key, if it is to be
+ * seen, has been appended: position n - 1), out = softmax(q . k^T / sqrt(head_dim)) . v
+ * with fp32 accumulation and softmax, stored in `dtype`.  n = 0 gives zeros.
+ * With a record, record[key] += sum over the G heads of the group of the key's softmax
+ * weight, for every visible key of every (sequence, KV head); a page that several
+ * sequences share receives all of their sums (in an order that is not fixed).
+ *
+ *   q           device [batch, h_q, 1, head_dim]
+ *   seq_len     device int32 [batch], 0..max_len
+ *   max_len     host, 1..max_pages * page_size
+ *   window      >= 1 (max_len or more: every key);  n_sink >= 0
+ *   record      device fp32 pool or NULL
+ *   out         device [batch, h_q, 1, head_dim]; must not alias an input
+ *   workspace   device scratch of paged_decode_attn_workspace_size(shape, max_len,
+ *               record != NULL) bytes; contents on entry ignored
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, CUDA.
+ */
+quoka_status paged_decode_attn(const quoka_paged_shape* shape, const void* q, const void* k_pages,
+                               const void* v_pages, const int32_t* block_table, const int32_t* seq_len,
+                               int max_len, int window, int n_sink, float* record, void* out,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* Bytes of device scratch paged_decode_attn() needs (0 if the arguments are invalid). */
+size_t paged_decode_attn_workspace_size(const quoka_paged_shape* shape, int max_len, int with_record);
+
+/*
+ * paged_evict - shrinks the cache of every sequence, each KV head by itself, to the rows
+ * that received the most attention weight.
+ *
+ * Of the n = seq_len[b] rows of (sequence b, KV head g), B = min(n, budget[b]) are kept:
+ * the first min(n_sink, B); of what is left of B, up to n_recent of the latest; and of the
+ * rows between, those with the largest record, ties to the lower position (a record that
+ * is NaN ranks with -infinity).  The kept rows of k_pages, v_pages and record are copied, in
+ * ascending order, to positions 0 .. B-1 of the pages of dst_table; the source pages and
+ * the slots behind position B-1 are left as they are.  The caller frees the old pages when
+ * the call's work is done, and goes on with dst_table and new_len.
+ *
+ *   budget      device int32 [batch], 0..b_max
+ *   b_max       host, 1..dst_max_pages * page_size: row length of idx_out
+ *   dst_table   device int32 [batch, dst_max_pages]; its pages that are written must not be
+ *               pages that the call reads, nor occur twice
+ *   n_sink, n_recent  >= 0
+ *   idx_out     device int32 [batch, h_kv, b_max]: the kept positions in ascending order,
+ *               then -1
+ *   new_len     device int32 [batch]: B
+ * max_len is at most QUOKA_MAX_EVICT_LEN.  Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+#define QUOKA_MAX_EVICT_LEN 786432
+quoka_status paged_evict(const quoka_paged_shape* shape, void* k_pages, void* v_pages, float* record,
+                         const int32_t* block_table, const int32_t* seq_len, int max_len,
+                         const int32_t* budget, int b_max, int n_sink, int n_recent,
+                         const int32_t* dst_table, int dst_max_pages, int32_t* idx_out, int32_t* new_len,
+                         void* stream);
+
+/*
  * quoka_select_noalloc - quoka_select without a caller-provided workspace.
  *
  * The paper has no counterpart to this call; it exists for callers that cannot
@@ -408,7 +544,7 @@ const char* quoka_last_error(void);
 
 /*
  * Reads and clears the device error word (0 = none): bit 0 a bounded wait gave up, bit 2
- * an index outside its range, bit 3 a per-query tile's union over max_union.
+ * an index, page or length outside its range, bit 3 a per-query tile's union over max_union.
  * Synchronises `stream`.  Returns QUOKA_ERR_CUDA if the read itself fails.
  */
 quoka_status quoka_device_error(uint32_t* code, void* stream);

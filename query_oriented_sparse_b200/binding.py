@@ -7,9 +7,10 @@ If the library is missing the first call raises: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
-from typing import Optional, Sequence
+from typing import List, Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -31,7 +32,14 @@ class QuokaShape(ctypes.Structure):
                 ("head_dim", ctypes.c_int), ("chunk", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class QuokaPagedShape(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("h_q", ctypes.c_int), ("h_kv", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("dtype", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("num_pages", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
 _SHAPE_P = ctypes.POINTER(QuokaShape)
+_PAGED_P = ctypes.POINTER(QuokaPagedShape)
 
 SIGNATURES = {
     "quoka_version": (ctypes.c_int, []),
@@ -69,6 +77,15 @@ SIGNATURES = {
                                              _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "sparse_chunk_attn_selcache": (ctypes.c_int, [_SHAPE_P, _P, _I32P, _I32P, _P, ctypes.c_int, _P,
                                                   _P, ctypes.c_size_t, _P]),
+    "window_chunk_attn_workspace_size": (ctypes.c_size_t, [_SHAPE_P, ctypes.c_int, ctypes.c_int]),
+    "window_chunk_attn": (ctypes.c_int, [_SHAPE_P, _P, _P, _P, _I64P, _I32P, ctypes.c_int, ctypes.c_int,
+                                         _P, _P, ctypes.c_size_t, _P]),
+    "paged_append": (ctypes.c_int, [_PAGED_P, _P, _P, ctypes.c_int, _P, _P, _P, _P, _P, _P, _P]),
+    "paged_decode_attn_workspace_size": (ctypes.c_size_t, [_PAGED_P, ctypes.c_int, ctypes.c_int]),
+    "paged_decode_attn": (ctypes.c_int, [_PAGED_P, _P, _P, _P, _P, _P, ctypes.c_int, ctypes.c_int,
+                                         ctypes.c_int, _P, _P, _P, ctypes.c_size_t, _P]),
+    "paged_evict": (ctypes.c_int, [_PAGED_P, _P, _P, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int,
+                                   ctypes.c_int, ctypes.c_int, _P, ctypes.c_int, _P, _P, _P]),
     "quoka_profile_events": (ctypes.c_int, [ctypes.POINTER(ctypes.c_void_p), ctypes.c_int]),
     "quoka_profile_marks": (ctypes.c_int, [ctypes.POINTER(ctypes.c_char_p), ctypes.c_int]),
 }
@@ -328,6 +345,258 @@ def quoka_prefill(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
         _ptr(v_cache), _host_i64(kv_off), int(nq), _host_i32(budgets), b_max, _ptr(idx),
         _ptr(out), _ptr(workspace), ws_bytes, ctypes.c_void_p(_stream(stream))))
     return out
+
+
+def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
+    """Context of a call on tensors of `dev`: that device current, and `stream` (when given)
+    the stream on which the call's outputs and scratch are allocated."""
+    if stream is not None:
+        if stream.device != dev:
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, f"the stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _need(name: str, t: torch.Tensor, shape: Tuple[int, ...], dtype: torch.dtype, dev: torch.device) -> None:
+    if t.shape != shape:
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if t.dtype != dtype:
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} is {t.dtype}, not {dtype}")
+    if t.device != dev:
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} is on {t.device}, not {dev}")
+    if not t.is_contiguous():
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} must be contiguous")
+
+
+def _scratch(workspace: Optional[torch.Tensor], n: int, dev: torch.device):
+    """(workspace, its bytes): the caller's, or a new one of n bytes (None for 0)."""
+    if workspace is None:
+        if n == 0:
+            return None, 0
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"workspace must be contiguous and on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _dims(t: torch.Tensor, name: str, n: int) -> Tuple[int, ...]:
+    if t.dim() != n:
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} must have {n} dimensions, not {t.dim()}")
+    return t.shape
+
+
+def window_workspace_size(shape: QuokaShape, max_prefix: int, window: int) -> int:
+    return int(lib().window_chunk_attn_workspace_size(ctypes.byref(shape), int(max_prefix), int(window)))
+
+
+def window_chunk_attn(q_chunk: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      kv_off: Sequence[int], prefix_len: Sequence[int], window: int, n_sink: int = 0,
+                      out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of the chunk over the latest `window` keys of each query and the first n_sink
+    tokens, over the contiguous cache; returns out [batch, h_q, C, d]."""
+    batch, _, _, d = _dims(q_chunk, "q_chunk", 4)
+    h_kv, rows, _ = _dims(k_cache, "k_cache", 3)
+    dev, dt = q_chunk.device, q_chunk.dtype
+    shape = shape_of(q_chunk, k_cache)
+    _need("q_chunk", q_chunk, q_chunk.shape, dt, dev)
+    _need("k_cache", k_cache, (h_kv, rows, d), dt, dev)
+    _need("v_cache", v_cache, (h_kv, rows, d), dt, dev)
+    if len(kv_off) != batch + 1 or len(prefix_len) != batch:
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, "kv_off needs batch + 1 entries, prefix_len batch")
+    if kv_off[batch] != rows:
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"the cache has {rows} rows, kv_off says {kv_off[batch]}")
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(q_chunk)
+        else:
+            _need("out", out, q_chunk.shape, dt, dev)
+        n = window_workspace_size(shape, max(prefix_len), window) if shape.chunk == 1 else 0
+        workspace, ws_bytes = _scratch(workspace, n, dev)
+        _check(lib().window_chunk_attn(
+            ctypes.byref(shape), _ptr(q_chunk), _ptr(k_cache), _ptr(v_cache), _host_i64(kv_off),
+            _host_i32(prefix_len), int(window), int(n_sink), _ptr(out), _ptr(workspace), ws_bytes,
+            ctypes.c_void_p(_stream(stream))))
+    return out
+
+
+def paged_shape(h_q: int, k_pages: torch.Tensor, block_table: torch.Tensor) -> QuokaPagedShape:
+    """The shape of a paged cache: pools [num_pages, h_kv, page_size, d], block_table
+    [batch, max_pages]."""
+    num_pages, h_kv, page, d = _dims(k_pages, "k_pages", 4)
+    batch, max_pages = _dims(block_table, "block_table", 2)
+    one = make_shape(batch, h_q, h_kv, d, 1, k_pages.dtype)
+    return QuokaPagedShape(batch, h_q, h_kv, d, one.dtype, page, num_pages, max_pages)
+
+
+def _need_pools(k_pages, v_pages, record, block_table, dev) -> None:
+    _need("k_pages", k_pages, k_pages.shape, k_pages.dtype, dev)
+    _need("v_pages", v_pages, k_pages.shape, k_pages.dtype, dev)
+    if record is not None:
+        _need("weight_pages", record, k_pages.shape[:3], torch.float32, dev)
+    _need("block_table", block_table, block_table.shape, torch.int32, dev)
+
+
+def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 block_table: torch.Tensor, start: torch.Tensor, n_new: Optional[torch.Tensor] = None,
+                 weight_pages: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> None:
+    """New K/V rows [batch, h_kv, n, d] of each sequence into its pages from position start[b]
+    (int32 [batch]); n_new, int32 [batch], limits the rows per sequence."""
+    dev = k_pages.device
+    shape = paged_shape(k_pages.shape[1] if k_pages.dim() == 4 else 1, k_pages, block_table)
+    _need_pools(k_pages, v_pages, weight_pages, block_table, dev)
+    n = _dims(k_new, "k_new", 4)[2]
+    want = (shape.batch, shape.h_kv, n, shape.head_dim)
+    _need("k_new", k_new, want, k_pages.dtype, dev)
+    _need("v_new", v_new, want, k_pages.dtype, dev)
+    _need("start", start, (shape.batch,), torch.int32, dev)
+    if n_new is not None:
+        _need("n_new", n_new, (shape.batch,), torch.int32, dev)
+    with _on(dev, stream):
+        _check(lib().paged_append(
+            ctypes.byref(shape), _ptr(k_new), _ptr(v_new), n, _ptr(k_pages), _ptr(v_pages),
+            _ptr(weight_pages), _ptr(block_table), _ptr(start), _ptr(n_new),
+            ctypes.c_void_p(_stream(stream))))
+
+
+def paged_decode_workspace_size(shape: QuokaPagedShape, max_len: int, with_record: bool) -> int:
+    return int(lib().paged_decode_attn_workspace_size(ctypes.byref(shape), int(max_len), int(with_record)))
+
+
+def paged_decode_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      block_table: torch.Tensor, seq_len: torch.Tensor, max_len: int,
+                      window: Optional[int] = None, n_sink: int = 0,
+                      weight_pages: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None,
+                      stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Attention of one new token per sequence, q [batch, h_q, 1, d], over its seq_len[b]
+    (int32, at most max_len) keys, or the latest `window` and the first n_sink of them.  With
+    weight_pages, each key's softmax weight, summed over its group's heads, is added there.
+    Returns out [batch, h_q, 1, d]."""
+    dev = k_pages.device
+    h_q = _dims(q, "q", 4)[1]
+    shape = paged_shape(h_q, k_pages, block_table)
+    _need_pools(k_pages, v_pages, weight_pages, block_table, dev)
+    _need("q", q, (shape.batch, h_q, 1, shape.head_dim), k_pages.dtype, dev)
+    _need("seq_len", seq_len, (shape.batch,), torch.int32, dev)
+    with _on(dev, stream):
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            _need("out", out, q.shape, q.dtype, dev)
+        workspace, ws_bytes = _scratch(
+            workspace, paged_decode_workspace_size(shape, max_len, weight_pages is not None)
+            if workspace is None else 0, dev)
+        _check(lib().paged_decode_attn(
+            ctypes.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_len),
+            int(max_len), int(max_len if window is None else window), int(n_sink), _ptr(weight_pages),
+            _ptr(out), _ptr(workspace), ws_bytes, ctypes.c_void_p(_stream(stream))))
+    return out
+
+
+def paged_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weight_pages: torch.Tensor,
+                block_table: torch.Tensor, seq_len: torch.Tensor, max_len: int, budget: torch.Tensor,
+                b_max: int, dst_table: torch.Tensor, n_sink: int = 0, n_recent: int = 0,
+                idx_out: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Copies, per sequence and KV head, the first n_sink, the n_recent latest and the heaviest
+    (by weight_pages) rows, budget[b] in all, to the pages of dst_table; returns the kept
+    positions [batch, h_kv, b_max] and the new lengths [batch]."""
+    dev = k_pages.device
+    shape = paged_shape(k_pages.shape[1] if k_pages.dim() == 4 else 1, k_pages, block_table)
+    _need_pools(k_pages, v_pages, weight_pages, block_table, dev)
+    _need("seq_len", seq_len, (shape.batch,), torch.int32, dev)
+    _need("budget", budget, (shape.batch,), torch.int32, dev)
+    dst_pages = _dims(dst_table, "dst_table", 2)[1]
+    _need("dst_table", dst_table, (shape.batch, dst_pages), torch.int32, dev)
+    with _on(dev, stream):
+        if idx_out is None:
+            idx_out = torch.empty(shape.batch, shape.h_kv, max(int(b_max), 1), dtype=torch.int32, device=dev)
+        else:
+            _need("idx_out", idx_out, (shape.batch, shape.h_kv, int(b_max)), torch.int32, dev)
+        if new_len is None:
+            new_len = torch.empty(shape.batch, dtype=torch.int32, device=dev)
+        else:
+            _need("new_len", new_len, (shape.batch,), torch.int32, dev)
+        _check(lib().paged_evict(
+            ctypes.byref(shape), _ptr(k_pages), _ptr(v_pages), _ptr(weight_pages), _ptr(block_table),
+            _ptr(seq_len), int(max_len), _ptr(budget), int(b_max), int(n_sink), int(n_recent),
+            _ptr(dst_table), dst_pages, _ptr(idx_out), _ptr(new_len), ctypes.c_void_p(_stream(stream))))
+    return idx_out, new_len
+
+
+class PagedCache:
+    """A paged KV cache of one layer: pools, block table, lengths and free pages for a fixed
+    batch, with the paged calls over them.  `record` adds the per-key weight record that
+    evict() goes by.  Pages are handed out on the host; the calls are stream-ordered."""
+
+    def __init__(self, batch: int, h_q: int, h_kv: int, head_dim: int, dtype: torch.dtype, num_pages: int,
+                 page_size: int, max_pages: int, device, record: bool = False):
+        self.h_q, self.page_size, self.max_pages = int(h_q), int(page_size), int(max_pages)
+        dev = torch.empty(0, device=device).device
+        self.k_pages = torch.zeros(num_pages, h_kv, page_size, head_dim, dtype=dtype, device=dev)
+        self.v_pages = torch.zeros_like(self.k_pages)
+        self.weight_pages = torch.zeros(num_pages, h_kv, page_size, device=dev) if record else None
+        self.lens: List[int] = [0] * batch
+        self.free: List[int] = list(range(num_pages - 1, -1, -1))
+        self.pages: List[List[int]] = [[] for _ in range(batch)]
+        self.block_table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=dev)
+        self.seq_len = torch.zeros(batch, dtype=torch.int32, device=dev)
+
+    def _take(self, counts: Sequence[int]) -> List[List[int]]:
+        if sum(counts) > len(self.free):
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{sum(counts)} pages needed, {len(self.free)} free")
+        return [[self.free.pop() for _ in range(n)] for n in counts]
+
+    def _table(self, pages: Sequence[Sequence[int]]) -> torch.Tensor:
+        rows = [list(p) + [-1] * (self.max_pages - len(p)) for p in pages]
+        return torch.tensor(rows, dtype=torch.int32).to(self.block_table.device)
+
+    def append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[Sequence[int]] = None) -> None:
+        """Appends k_new / v_new [batch, h_kv, n, d], or the first counts[b] rows of each."""
+        n = int(k_new.shape[2])
+        add = [n] * len(self.lens) if counts is None else [int(c) for c in counts]
+        if len(add) != len(self.lens) or any(c < 0 or c > n for c in add):
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, "counts needs one entry in [0, n] per sequence")
+        more = [-(-(l + c) // self.page_size) - len(p) for l, c, p in zip(self.lens, add, self.pages)]
+        if any(len(p) + m > self.max_pages for p, m in zip(self.pages, more)):
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, "a sequence would need more than max_pages pages")
+        if any(more):
+            self.pages = [p + m for p, m in zip(self.pages, self._take(more))]
+            self.block_table = self._table(self.pages)
+        cnt = None if counts is None else torch.tensor(add, dtype=torch.int32).to(self.seq_len.device)
+        paged_append(k_new, v_new, self.k_pages, self.v_pages, self.block_table, self.seq_len, n_new=cnt,
+                     weight_pages=self.weight_pages)
+        self.seq_len = self.seq_len + (n if cnt is None else cnt)
+        self.lens = [l + c for l, c in zip(self.lens, add)]
+
+    def attend(self, q: torch.Tensor, window: Optional[int] = None, n_sink: int = 0) -> torch.Tensor:
+        """One new token per sequence, q [batch, h_q, 1, d]; adds to the record if there is one."""
+        return paged_decode_attn(q, self.k_pages, self.v_pages, self.block_table, self.seq_len,
+                                 max(max(self.lens), 1), window=window, n_sink=n_sink,
+                                 weight_pages=self.weight_pages)
+
+    def evict(self, budget: Union[int, Sequence[int]], n_sink: int = 0, n_recent: int = 0) -> torch.Tensor:
+        """Shrinks every sequence to its budget; returns the kept positions of each KV head."""
+        if self.weight_pages is None:
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, "this cache keeps no weight record")
+        want = [int(budget)] * len(self.lens) if isinstance(budget, int) else [int(b) for b in budget]
+        if len(want) != len(self.lens) or any(b < 0 for b in want):
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, "budget needs one entry >= 0 per sequence")
+        keep = [min(l, b) for l, b in zip(self.lens, want)]
+        pages = self._take([-(-k // self.page_size) for k in keep])
+        table = self._table(pages)
+        dev = table.device
+        idx, new_len = paged_evict(self.k_pages, self.v_pages, self.weight_pages, self.block_table, self.seq_len,
+                                   max(max(self.lens), 1), torch.tensor(keep, dtype=torch.int32).to(dev),
+                                   max(max(keep), 1), table, n_sink=n_sink, n_recent=n_recent)
+        for p in self.pages:
+            self.free.extend(p)
+        self.pages, self.block_table, self.seq_len, self.lens = pages, table, new_len, keep
+        return idx
 
 
 def device_error(stream: Optional[torch.cuda.Stream] = None) -> int:

@@ -1,0 +1,422 @@
+// Attention of one new token per sequence over its whole cache or a window of it, for a
+// paged or a contiguous cache: out = softmax(q . k^T / sqrt(d)) . v over the visible keys
+// j < n with j < n_sink or j >= n - window, n the sequence's tokens.
+//
+// The keys are read once and little is computed with each, so the kernel is bound by HBM.
+// What matters is that every SM reads all the time, whatever the batch looks like.  So
+// the work is cut by bytes, not by sequence: the visible keys of every (sequence, KV head)
+// are counted in 128-key tiles, and CTA c of N takes tiles [c T / N, (c+1) T / N) of the
+// list of all T, crossing sequences where the cut falls.  The lengths are read on the
+// device, so a captured graph serves growing sequences.  A (sequence, KV head) that one
+// CTA holds whole is finished there; one that several share leaves at most one partial
+// (running maximum, sum and output, fp32) per CTA, two slots in all, and the join kernel
+// merges them.  With a weight record, the logits are kept (fp32, base 2) and the record
+// kernel adds each key's softmax weight, summed over the group's heads, once the join has
+// the row's maximum and sum.
+//
+// This file: the split, the CUDA-core kernel (fp32), the join and the record kernel.
+#pragma once
+#include "attn_decode.cuh"
+#include "kv_pages.cuh"
+
+namespace quoka {
+
+constexpr int AST_TILE = 128;             // keys per tile
+constexpr int AST_MAX_BATCH = 1024;
+
+// Visible key tiles of one sequence: nst tiles of first tokens, then tiles wt0 onwards.
+struct KeySpan {
+  int n, ns, lo;                          // visible: j < n and (j < ns or j >= lo)
+  int nst, wt0, nt;
+
+  __device__ __forceinline__ bool visible(int j) const { return j < n && (j < ns || j >= lo); }
+  __device__ __forceinline__ int tile(int i) const { return i < nst ? i : i - nst + wt0; }
+};
+
+// An empty sequence has one tile without visible keys, so its (zero) output is written.
+__device__ __forceinline__ KeySpan key_span(int n, int window, int n_sink) {
+  KeySpan s;
+  s.n = n;
+  s.ns = min(n_sink, n);
+  s.lo = max(0, n - window);
+  if (s.ns >= s.lo) s.ns = s.lo = 0;
+  s.nst = (s.ns + AST_TILE - 1) / AST_TILE;
+  s.wt0 = max(s.lo / AST_TILE, s.nst);
+  s.nt = max(1, s.nst + (n + AST_TILE - 1) / AST_TILE - s.wt0);
+  return s;
+}
+
+struct StreamParams {
+  KvView kv;
+  int batch, h_q, h_kv, G;
+  int window, n_sink;
+  float scale_log2;                       // log2(e) / sqrt(d)
+  int ctas;                               // N at most (the tiles, when they are fewer)
+  float* part;                            // [2 N][G][D] partial outputs
+  float* part_ml;                         // [2 N][G][2] their running maximum (base 2) and sum
+  float* unit_ml;                         // [batch * h_kv][G][2] maximum and 1 / sum (with a record)
+  float* logits;                          // [tile][128][G] or NULL
+  float* record;
+};
+
+template <bool kPaged>
+__device__ __forceinline__ int stream_len(const StreamParams& p, const SeqTable& tab, int b) {
+  if constexpr (kPaged) return paged_len(p.kv.seq_len, b, p.kv.max_len);
+  else return tab.prefix[b] + 1;
+}
+
+// base[b] = tiles of one KV head of the sequences before b; base[batch] the total.
+// Every thread of the block calls it.
+template <bool kPaged>
+__device__ void stream_bases(const StreamParams& p, const SeqTable& tab, int* base) {
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
+    base[b + 1] = key_span(stream_len<kPaged>(p, tab, b), p.window, p.n_sink).nt;
+  if (threadIdx.x == 0) base[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    int run = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + threadIdx.x;
+      int x = b < p.batch ? base[b + 1] : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if ((int)threadIdx.x >= o) x += y;
+      }
+      x += run;
+      if (b < p.batch) base[b + 1] = x;
+      run = __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ int stream_start(int c, int ctas, int tiles) {
+  return (int)((long long)c * tiles / ctas);
+}
+__device__ __forceinline__ int stream_cta(int tile, int ctas, int tiles) {
+  return (int)((((long long)tile + 1) * ctas - 1) / tiles);
+}
+// Sequence that tile x of the list belongs to.
+__device__ __forceinline__ int stream_seq(const int* base, int batch, int h_kv, int x) {
+  int lo = 0, hi = batch - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((long long)base[mid] * h_kv <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// A run of tiles of one (sequence, KV head) inside a CTA's share.
+struct StreamSeg {
+  int b, g, unit, i0, cnt;                // tiles i0 .. i0 + cnt - 1 of the unit's nt
+  bool whole;
+  KeySpan span;
+};
+template <bool kPaged>
+__device__ __forceinline__ StreamSeg stream_seg(const StreamParams& p, const SeqTable& tab, const int* base, int x,
+                                                int x1) {
+  StreamSeg s;
+  s.b = stream_seq(base, p.batch, p.h_kv, x);
+  s.span = key_span(stream_len<kPaged>(p, tab, s.b), p.window, p.n_sink);
+  const int r = x - base[s.b] * p.h_kv;
+  s.g = r / s.span.nt;
+  s.i0 = r - s.g * s.span.nt;
+  s.unit = s.b * p.h_kv + s.g;
+  s.cnt = min(s.span.nt - s.i0, x1 - x);
+  s.whole = s.cnt == s.span.nt;
+  return s;
+}
+
+// Row of position j in the K/V pools or cache, -1 for none.
+template <bool kPaged>
+__device__ __forceinline__ long long stream_row(const StreamParams& p, const SeqTable& tab, int b, int g, int j) {
+  if constexpr (kPaged) return paged_row(p.kv, b, g, p.h_kv, j);
+  else return (long long)g * p.kv.rows_per_head + tab.kv_off[b] + j;
+}
+
+// 16-byte asynchronous copy, or 16 zero bytes when `on` is false (nothing is read then).
+__device__ __forceinline__ void ast_cp16(void* dst, const void* src, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "r"(on ? 16 : 0)
+               : "memory");
+}
+
+template <typename T, int D, int R>
+constexpr int ast_smem_bytes(int batch) {
+  return adc_smem_bytes<T, D, R>() + (batch + 1) * 4;
+}
+
+// CUDA-core form (fp32).  Warps take 32-key batches of the CTA's tiles in turn, each with
+// its own stage in shared memory: lane l owns key l for the logits, then head dims
+// [EPL l, EPL l + EPL) for P.V, as in attn_decode.cuh.  Rows of keys that are not visible
+// are filled with zeros instead of read.  blockIdx.y: query heads R y .. of each group.
+template <typename T, int D, int R, bool kPaged>
+__global__ void __launch_bounds__(AdcCfg<T, D>::THREADS)
+attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __restrict__ v,
+                   const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab,
+                   T* __restrict__ out) {
+  using Cfg = AdcCfg<T, D>;
+  constexpr int NW = Cfg::NW, ROW = Cfg::ROW, VPR = Cfg::VPR, EPV = Cfg::EPV, EPL = Cfg::EPL;
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float* qs = reinterpret_cast<float*>(smem);              // [R][D], times scale * log2(e)
+  float* mls = qs + R * D;                                 // [NW][R][2]
+  unsigned char* stage = smem + (R * D + NW * R * 2) * 4 + warp * (Cfg::STAGE + 32 * R * 4);
+  unsigned char* vstage = stage + 32 * ROW;
+  float* ps = reinterpret_cast<float*>(stage + Cfg::STAGE);
+  int* base = reinterpret_cast<int*>(smem + adc_smem_bytes<T, D, R>());
+  stream_bases<kPaged>(p, tab, base);
+
+  const int tiles = base[p.batch] * p.h_kv;
+  const int ctas = min(p.ctas, tiles);                     // every share holds a tile at least
+  const int c = blockIdx.x, r0 = blockIdx.y * R;
+  if (c >= ctas) return;
+  const int rows = min(R, p.G - r0);
+  const int x0 = stream_start(c, ctas, tiles), x1 = stream_start(c + 1, ctas, tiles);
+  for (int x = x0; x < x1;) {
+    const StreamSeg sg = stream_seg<kPaged>(p, tab, base, x, x1);
+    for (int e = threadIdx.x; e < R * D; e += blockDim.x) {
+      const int r = e / D, d = e - r * D;
+      qs[e] = r < rows ? to_f32(q[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + r0 + r) * D + d]) * p.scale_log2 : 0.f;
+    }
+    __syncthreads();
+    float m[R], l[R], acc[R][EPL];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[r][e] = 0.f;
+    }
+    for (int w = warp; w < sg.cnt * 4; w += NW) {          // 32-key batches of the segment
+      const int j = sg.span.tile(sg.i0 + (w >> 2)) * AST_TILE + (w & 3) * 32 + lane;
+      bool vis = sg.span.visible(j);
+      int row = 0;
+      if (vis) {
+        const long long rr = stream_row<kPaged>(p, tab, sg.b, sg.g, j);
+        row = rr < 0 ? 0 : (int)rr;                        // pools and caches hold fewer than 2^31 rows
+        if (rr < 0) vis = false;
+      }
+      const unsigned on = __ballot_sync(0xffffffffu, vis);
+      float sc[R];
+      if (on) {
+#pragma unroll 4
+        for (int e = lane; e < 32 * VPR; e += 32) {
+          const int kk = e / VPR, vv = e - kk * VPR;
+          const int rk = __shfl_sync(0xffffffffu, row, kk);
+          ast_cp16(stage + kk * ROW + vv * 16, k + (size_t)rk * D + vv * EPV, (on >> kk) & 1u);
+        }
+        adc_commit();
+#pragma unroll 4
+        for (int e = lane; e < 32 * VPR; e += 32) {
+          const int kk = e / VPR, vv = e - kk * VPR;
+          const int rk = __shfl_sync(0xffffffffu, row, kk);
+          ast_cp16(vstage + kk * ROW + vv * 16, v + (size_t)rk * D + vv * EPV, (on >> kk) & 1u);
+        }
+        adc_commit();
+        adc_wait<1>();
+        __syncwarp();
+#pragma unroll
+        for (int r = 0; r < R; ++r) sc[r] = 0.f;
+        const unsigned char* krow = stage + lane * ROW;
+#pragma unroll 2
+        for (int cc = 0; cc < VPR; ++cc) {
+          float kx[EPV];
+          smem_vec16<T>(krow + cc * 16, kx);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
+            const float* qr = qs + r * D + cc * EPV;
+#pragma unroll
+            for (int e4 = 0; e4 < EPV; e4 += 4) {
+              const float4 qv = *reinterpret_cast<const float4*>(qr + e4);
+              sc[r] = fmaf(qv.x, kx[e4], sc[r]);
+              sc[r] = fmaf(qv.y, kx[e4 + 1], sc[r]);
+              sc[r] = fmaf(qv.z, kx[e4 + 2], sc[r]);
+              sc[r] = fmaf(qv.w, kx[e4 + 3], sc[r]);
+            }
+          }
+        }
+      }
+      if (!vis) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) sc[r] = -INFINITY;
+      }
+      if (p.logits) {
+        float* lg = p.logits + ((size_t)(x + (w >> 2)) * AST_TILE + (w & 3) * 32 + lane) * p.G + r0;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          if (r < rows) lg[r] = sc[r];
+      }
+      if (!on) continue;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float mx = sc[r];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const float mn = fmaxf(m[r], mx);
+        float pr = 0.f, corr = 1.f;
+        if (mn != -INFINITY) {
+          pr = exp2f(sc[r] - mn);
+          corr = exp2f(m[r] - mn);
+        }
+        float sum = pr;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        l[r] = l[r] * corr + sum;
+        m[r] = mn;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[r][e] *= corr;
+        ps[lane * R + r] = pr;
+      }
+      adc_wait<0>();
+      __syncwarp();
+      for (int kk = 0; kk < 32; ++kk) {
+        float vx[EPL];
+        smem_vecn<T, EPL>(vstage + kk * ROW + lane * EPL * Cfg::ESZ, vx);
+        const float* pk = ps + kk * R;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float pr = pk[r];
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) acc[r][e] = fmaf(pr, vx[e], acc[r][e]);
+        }
+      }
+      __syncwarp();                                        // stage free for the next batch
+    }
+
+    // merge the warps of the CTA
+    float* wout = reinterpret_cast<float*>(stage);
+    if (lane == 0) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        mls[(warp * R + r) * 2] = m[r];
+        mls[(warp * R + r) * 2 + 1] = l[r];
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) wout[r * D + lane * EPL + e] = acc[r][e];
+    __syncthreads();
+    const int slot = 2 * c + (x == x0 ? 0 : 1);
+    for (int e = threadIdx.x; e < rows * D; e += blockDim.x) {
+      const int r = e / D, d = e - r * D;
+      float M = -INFINITY, L = 0.f, o = 0.f;
+#pragma unroll
+      for (int w = 0; w < NW; ++w) M = fmaxf(M, mls[(w * R + r) * 2]);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float mw = mls[(w * R + r) * 2], lw = mls[(w * R + r) * 2 + 1];
+        const float* ww = reinterpret_cast<const float*>(smem + (R * D + NW * R * 2) * 4 +
+                                                         w * (Cfg::STAGE + 32 * R * 4));
+        if (lw != 0.f) {                                   // a warp without visible keys adds nothing
+          const float f = exp2f(mw - M);
+          o = fmaf(ww[e], f, o);
+          L = fmaf(lw, f, L);
+        }
+      }
+      if (sg.whole) {
+        out[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + r0 + r) * D + d] = from_f32<T>(L == 0.f ? 0.f : o / L);
+        if (d == 0 && p.logits) {
+          p.unit_ml[((size_t)sg.unit * p.G + r0 + r) * 2] = M;
+          p.unit_ml[((size_t)sg.unit * p.G + r0 + r) * 2 + 1] = L == 0.f ? 0.f : 1.f / L;
+        }
+      } else {
+        p.part[((size_t)slot * p.G + r0 + r) * D + d] = o;
+        if (d == 0) {
+          p.part_ml[((size_t)slot * p.G + r0 + r) * 2] = M;
+          p.part_ml[((size_t)slot * p.G + r0 + r) * 2 + 1] = L;
+        }
+      }
+    }
+    __syncthreads();                                       // qs, mls and the stages are free
+    x += sg.cnt;
+  }
+}
+
+constexpr int ASJ_THREADS = 256;
+
+// Slot of CTA c's partial of a unit whose tiles start at s: the CTA's first segment when
+// its share starts inside the unit, else its last.
+__device__ __forceinline__ int stream_slot(int c, int s, int ctas, int tiles) {
+  return 2 * c + (stream_start(c, ctas, tiles) >= s ? 0 : 1);
+}
+
+// One block per (sequence, KV head): out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M).
+template <typename T, int D, bool kPaged>
+__global__ void __launch_bounds__(ASJ_THREADS)
+attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab,
+                        T* __restrict__ out) {
+  extern __shared__ int base[];                            // [batch + 1], then weights [N][G]
+  stream_bases<kPaged>(p, tab, base);
+  const int tiles = base[p.batch] * p.h_kv, ctas = min(p.ctas, tiles);
+  const int unit = blockIdx.x, b = unit / p.h_kv, g = unit - b * p.h_kv;
+  const int nt = base[b + 1] - base[b];
+  const int s = base[b] * p.h_kv + g * nt;
+  const int c0 = stream_cta(s, ctas, tiles), c1 = stream_cta(s + nt - 1, ctas, tiles);
+  if (c0 == c1) return;                                    // finished by its CTA
+  const int nc = c1 - c0 + 1;
+  float* fw = reinterpret_cast<float*>(base + p.batch + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int r = warp; r < p.G; r += ASJ_THREADS / 32) {
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane; i < nc; i += 32) {
+      const float* ml = p.part_ml + ((size_t)stream_slot(c0 + i, s, ctas, tiles) * p.G + r) * 2;
+      if (ml[1] != 0.f) M = fmaxf(M, ml[0]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int i = lane; i < nc; i += 32) {
+      const float* ml = p.part_ml + ((size_t)stream_slot(c0 + i, s, ctas, tiles) * p.G + r) * 2;
+      const float f = ml[1] != 0.f ? exp2f(ml[0] - M) : 0.f;   // a partial without visible keys weighs 0
+      fw[i * p.G + r] = f;
+      L += ml[1] * f;
+    }
+    L = warp_sum(L);
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    for (int i = lane; i < nc; i += 32) fw[i * p.G + r] *= inv;
+    if (lane == 0 && p.logits) {
+      p.unit_ml[((size_t)unit * p.G + r) * 2] = M;
+      p.unit_ml[((size_t)unit * p.G + r) * 2 + 1] = inv;
+    }
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < p.G * D; e += ASJ_THREADS) {
+    const int r = e / D, d = e - r * D;
+    float o = 0.f;
+    for (int i0 = 0; i0 < nc; i0 += 8) {
+      float xs[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        xs[u] = i0 + u < nc ? p.part[((size_t)stream_slot(c0 + i0 + u, s, ctas, tiles) * p.G + r) * D + d] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (i0 + u < nc && fw[(i0 + u) * p.G + r] != 0.f) o = fmaf(xs[u], fw[(i0 + u) * p.G + r], o);
+    }
+    out[((size_t)b * p.h_q + (size_t)g * p.G + r) * D + d] = from_f32<T>(o);
+  }
+}
+
+// record[key] += sum over the group's heads of 2^(s - M) / L.  One thread per key of a tile.
+// The add is a reduction in memory, so a page that two sequences share gets both sums.
+__global__ void __launch_bounds__(AST_TILE)
+attn_stream_record_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab) {
+  extern __shared__ int base[];
+  stream_bases<true>(p, tab, base);
+  const int tiles = base[p.batch] * p.h_kv;
+  for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
+    const StreamSeg sg = stream_seg<true>(p, tab, base, x, x + 1);
+    const int j = sg.span.tile(sg.i0) * AST_TILE + threadIdx.x;
+    if (!sg.span.visible(j)) continue;
+    const float* lg = p.logits + ((size_t)x * AST_TILE + threadIdx.x) * p.G;
+    const float* ml = p.unit_ml + (size_t)sg.unit * p.G * 2;
+    float w = 0.f;
+    for (int r = 0; r < p.G; ++r) w += exp2f(lg[r] - ml[2 * r]) * ml[2 * r + 1];
+    const long long row = paged_row(p.kv, sg.b, sg.g, p.h_kv, j);
+    if (row >= 0) atomicAdd(p.record + row, w);
+  }
+}
+
+}  // namespace quoka

@@ -1,0 +1,169 @@
+// A paged KV cache: pools of pages k / v [num_pages][h_kv][page_size][head_dim] and, per
+// key and KV head, a record of accumulated attention weight [num_pages][h_kv][page_size]
+// (fp32).  Position j of sequence b lies in page block_table[b][j / page_size], slot
+// j % page_size.  This file holds the addressing and the two operators that move rows:
+//
+//   paged_append_kernel  new rows into the pages; a copy, bound by its bytes (or, for one
+//                        token per sequence, by the launch).
+//   evict_select_kernel  the rows to keep, per (sequence, KV head): the first `first` and
+//                        the last `last` rows, and of the rest those with the most weight,
+//                        ties to the lower position.  A radix select (cluster_select.cuh)
+//                        over the rest of the sequence, ascending output without a sort.
+//   evict_copy_kernel    the kept rows and their records, in order, into other pages.
+#pragma once
+#include "cluster_select.cuh"
+
+namespace quoka {
+
+// Where the K/V rows of (sequence, KV head, position) lie.  seq_len, block_table: paged
+// (device memory); rows_per_head and a SeqTable: the contiguous cache.
+struct KvView {
+  const int32_t* seq_len;
+  const int32_t* block_table;
+  int max_pages, page_size, num_pages;
+  int max_len;                     // the caller's bound on seq_len
+  long long rows_per_head;
+};
+
+// Tokens of sequence b, held to [0, bound] (a length outside is reported).
+__device__ __forceinline__ int paged_len(const int32_t* seq_len, int b, int bound) {
+  const int n = __ldg(seq_len + b);
+  if (n >= 0 && n <= bound) return n;
+  flag_error(ERR_BAD_INDEX);
+  return n < 0 ? 0 : bound;
+}
+
+// Page of position j of sequence b, or -1 (reported) when the table holds none there.
+__device__ __forceinline__ int page_of(const KvView& kv, int b, int j, int* slot) {
+  const int p = j / kv.page_size;
+  *slot = j - p * kv.page_size;
+  const int page = __ldg(kv.block_table + (size_t)b * kv.max_pages + p);
+  if (page >= 0 && page < kv.num_pages) return page;
+  flag_error(ERR_BAD_INDEX);
+  return -1;
+}
+
+// Row (of head_dim elements) of position j in a pool; -1 when its page is bad.
+__device__ __forceinline__ long long paged_row(const KvView& kv, int b, int g, int h_kv, int j) {
+  int slot;
+  const int page = page_of(kv, b, j, &slot);
+  return page < 0 ? -1 : ((long long)page * h_kv + g) * kv.page_size + slot;
+}
+
+constexpr int PAGED_THREADS = 256;
+
+// New rows k_new / v_new [batch][h_kv][n_new][D] of sequence b to positions start[b] + t,
+// t < count[b] (all n_new when count is NULL).  One thread per 16-byte vector of a row.
+// A row whose position has no page is reported and not written.
+__global__ void __launch_bounds__(PAGED_THREADS)
+paged_append_kernel(const uint4* __restrict__ k_new, const uint4* __restrict__ v_new, uint4* __restrict__ k,
+                    uint4* __restrict__ v, float* __restrict__ record, const KvView kv,
+                    const int32_t* __restrict__ start, const int32_t* __restrict__ count, int h_kv, int n_new,
+                    int vpr, long long total) {
+  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < total;
+       e += (long long)gridDim.x * blockDim.x) {
+    const long long row = e / vpr;
+    const int vec = (int)(e - row * vpr);
+    const long long bg = row / n_new;
+    const int t = (int)(row - bg * n_new);
+    const int b = (int)(bg / h_kv), g = (int)(bg - (long long)b * h_kv);
+    if (count && t >= paged_len(count, b, n_new)) continue;
+    const long long at = (long long)__ldg(start + b) + t;
+    if (at < 0 || at >= (long long)kv.max_pages * kv.page_size) {
+      flag_error(ERR_BAD_INDEX);
+      continue;
+    }
+    const long long dst = paged_row(kv, b, g, h_kv, (int)at);
+    if (dst < 0) continue;
+    k[dst * vpr + vec] = __ldg(k_new + e);
+    v[dst * vpr + vec] = __ldg(v_new + e);
+    if (record && vec == 0) record[dst] = 0.f;
+  }
+}
+
+// How many rows sequence b keeps, and how many of them are its first and its latest ones:
+// the first rows come first, then the latest, then the rest by weight.
+struct EvictSplit {
+  int n, kept, first, last;
+};
+__device__ __forceinline__ EvictSplit evict_split(const KvView& kv, const int32_t* budget, int b, int b_max,
+                                                  int n_sink, int n_recent) {
+  EvictSplit s;
+  s.n = paged_len(kv.seq_len, b, kv.max_len);
+  s.kept = min(s.n, paged_len(budget, b, b_max));
+  s.first = min(n_sink, s.kept);
+  s.last = min(n_recent, s.kept - s.first);
+  return s;
+}
+
+constexpr int EVS_THREADS = 512;
+constexpr int EVS_MAX_CS = 16;
+constexpr int EVS_STAGE_KEYS = 49152;          // candidate keys a CTA stages (192 KB)
+
+// One cluster of CS CTAs per (sequence, KV head).
+template <int CS>
+__global__ void __cluster_dims__(CS, 1, 1) __launch_bounds__(EVS_THREADS)
+evict_select_kernel(const float* __restrict__ record, const KvView kv, const int32_t* __restrict__ budget,
+                    int h_kv, int b_max, int n_sink, int n_recent, int32_t* __restrict__ idx_out,
+                    int32_t* __restrict__ new_len) {
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ SelectSmem sm;
+  extern __shared__ uint32_t staged[];
+
+  const int rank = (int)cluster.block_rank();
+  const int head = blockIdx.x / CS;
+  const int b = head / h_kv, g = head - b * h_kv;
+  const EvictSplit s = evict_split(kv, budget, b, b_max, n_sink, n_recent);
+  int32_t* out = idx_out + (size_t)head * b_max;
+  const int t0 = rank * blockDim.x + threadIdx.x, stride = CS * blockDim.x;
+  if (g == 0 && t0 == 0) new_len[b] = s.kept;
+  for (int i = s.kept + t0; i < b_max; i += stride) out[i] = -1;
+  if (s.kept == s.n) {                         // everything stays
+    for (int i = t0; i < s.n; i += stride) out[i] = i;
+    return;
+  }
+  for (int i = t0; i < s.first; i += stride) out[i] = i;
+  for (int i = t0; i < s.last; i += stride) out[s.kept - s.last + i] = s.n - s.last + i;
+  const int take = s.kept - s.first - s.last;  // of the n - first - last candidates (more than take)
+  if (take == 0) return;
+
+  const int cand = s.n - s.first - s.last;
+  const int per = (cand + CS - 1) / CS;
+  const int lo = min(cand, rank * per), hi = min(cand, lo + per);
+  // the slice's weights as ordered keys; NaN ranks with -inf, behind every number
+  for (int j = lo + threadIdx.x; j < hi; j += blockDim.x) {
+    const long long row = paged_row(kv, b, g, h_kv, s.first + j);
+    const float w = row < 0 ? -INFINITY : __ldg(record + row);
+    staged[j - lo] = float_to_ordered(w == w ? w : -INFINITY);
+  }
+  __syncthreads();
+  auto key_at = [&](int j) { return staged[j - lo]; };
+  const SelectThreshold th = cluster_threshold<CS, true>(cluster, sm, key_at, lo, hi, take);
+  ordered_emit<true>(sm, key_at, lo, hi, th, [&](int pos, int j) {
+    if (pos < take) out[s.first + pos] = s.first + j;
+    else flag_error(ERR_BAD_INDEX);            // unreachable when the counts are consistent
+  });
+  cluster_wait();                              // peers' last reads of this CTA's histograms
+}
+
+// Kept row i of (b, g), position idx[i], to position i of dst (its own table).
+__global__ void __launch_bounds__(PAGED_THREADS)
+evict_copy_kernel(uint4* __restrict__ k, uint4* __restrict__ v, float* __restrict__ record, const KvView kv,
+                  const KvView dst, const int32_t* __restrict__ idx, const int32_t* __restrict__ new_len,
+                  int h_kv, int b_max, int vpr) {
+  const int head = blockIdx.x;
+  const int b = head / h_kv, g = head - b * h_kv;
+  const int kept = new_len[b];
+  const int total = kept * vpr;
+  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < total; e += gridDim.y * blockDim.x) {
+    const int i = e / vpr, vec = e - i * vpr;
+    const long long from = paged_row(kv, b, g, h_kv, idx[(size_t)head * b_max + i]);
+    const long long to = paged_row(dst, b, g, h_kv, i);
+    if (from < 0 || to < 0) continue;
+    k[to * vpr + vec] = k[from * vpr + vec];
+    v[to * vpr + vec] = v[from * vpr + vec];
+    if (vec == 0) record[to] = record[from];
+  }
+}
+
+}  // namespace quoka

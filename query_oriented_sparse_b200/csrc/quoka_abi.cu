@@ -4,6 +4,8 @@
 #include <algorithm>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
+#include <exception>
 #include <map>
 #include <mutex>
 #include <string>
@@ -25,6 +27,8 @@
 #include "attn_perq.cuh"
 #include "selcache.cuh"
 #include "perq_tc.cuh"
+#include "attn_window.cuh"
+#include "attn_stream.cuh"
 
 using namespace quoka;
 
@@ -1526,3 +1530,5 @@ quoka_status quoka_device_error(uint32_t* code, void* stream) {
 }
 
 }  // extern "C"
+
+#include "paged_abi.cuh"
