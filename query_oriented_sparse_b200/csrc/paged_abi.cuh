@@ -180,6 +180,72 @@ quoka_status launch_window_simt(const Dims& d, const SeqTable& tab, long long ro
   return QUOKA_OK;
 }
 
+// Clusters (SM pairs) of the window kernel that fit on the device at once.
+int window_resident_pairs(int smem) {
+  static std::mutex mu;
+  static std::map<int, int> cache;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  std::lock_guard<std::mutex> lock(mu);
+  auto it = cache.find(dev);
+  if (it != cache.end()) return it->second;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * sm_count(), 1, 1);
+  cfg.blockDim = dim3(AT2_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, (const void*)window_tc2_kernel, &cfg) != cudaSuccess || n <= 0) {
+    (void)cudaGetLastError();
+    n = sm_count() / 2;
+  }
+  cache[dev] = n;
+  return n;
+}
+
+// bf16: 128-row query tiles, the G heads of a KV head at 128 / G positions each, two to a tile.
+template <int D>
+quoka_status launch_window_tc(const Dims& d, const SeqTable& tab, long long rows, const void* q, const void* k,
+                              const void* v, int window, int n_sink, void* out, cudaStream_t st) {
+  WindowTcParams p;
+  p.h_q = d.h_q;
+  p.h_kv = d.h_kv;
+  p.G = d.G;
+  p.C = d.C;
+  p.TP = 128 / d.G;
+  p.window = window;
+  p.n_sink = n_sink;
+  p.rows_per_head = rows;
+  p.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+  CUtensorMap qmap, kmap, vmap;
+  quoka_status s;
+  const uint64_t kv_rows = (uint64_t)d.h_kv * rows;
+  if ((s = make_map_bf16(&qmap, q, (uint64_t)d.batch * d.h_q * d.C, D, 64, 1, "q_chunk")) != QUOKA_OK) return s;
+  if ((s = make_map_bf16(&kmap, k, kv_rows, D, 64, D == 128 ? 64 : 128, "k_cache")) != QUOKA_OK) return s;
+  if ((s = make_map_bf16(&vmap, v, kv_rows, D, 64, 128, "v_cache")) != QUOKA_OK) return s;
+  const int npairs = (d.C + 2 * p.TP - 1) / (2 * p.TP);
+  const long long tiles = (long long)npairs * d.h_kv * d.batch;
+  if (tiles >= (1ll << 31)) return fail(QUOKA_ERR_UNSUPPORTED, "more than 2^31 query tiles");
+  cudaError_t e;
+  if constexpr (D == 128) {
+    const int smem = AwtCfg::SMEM;
+    if ((e = ensure_smem(window_tc2_kernel, smem)) != cudaSuccess) return cuda_fail(e, "window_tc2 smem");
+    const int ncl = (int)std::min<long long>(tiles, window_resident_pairs(smem));
+    window_tc2_kernel<<<dim3(2 * ncl), AT2_THREADS, smem, st>>>(qmap, kmap, vmap, tab, p,
+                                                                 reinterpret_cast<const __nv_bfloat16*>(v),
+                                                                 reinterpret_cast<__nv_bfloat16*>(out));
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_tc2 launch");
+    prof_mark(st, "window_tc2_kernel");
+  } else {
+    const int smem = AtcCfg<D>::SMEM + 16;
+    if ((e = ensure_smem(window_tc_kernel, smem)) != cudaSuccess) return cuda_fail(e, "window_tc smem");
+    window_tc_kernel<<<dim3(npairs, d.h_kv, d.batch), ATC_THREADS, smem, st>>>(
+        qmap, kmap, vmap, tab, p, reinterpret_cast<const __nv_bfloat16*>(v), reinterpret_cast<__nv_bfloat16*>(out));
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_tc launch");
+    prof_mark(st, "window_tc_kernel");
+  }
+  return QUOKA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -227,8 +293,8 @@ quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, co
     if (d.dt == QUOKA_F32)
       return d.D == 64 ? launch_window_simt<float, 64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
                        : launch_window_simt<float, 128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
-    return d.D == 64 ? launch_window_simt<__nv_bfloat16, 64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
-                     : launch_window_simt<__nv_bfloat16, 128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
+    return d.D == 64 ? launch_window_tc<64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
+                     : launch_window_tc<128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
   });
 }
 
