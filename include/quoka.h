@@ -365,7 +365,8 @@ quoka_status sparse_chunk_attn_selcache(const quoka_shape* shape, const void* q_
  * at least its own key.  Rows of the cache that no query sees are not used, and what a key
  * or value holds reaches only the queries that see it, infinities and NaN included.
  * chunk = 1 (a decode step) runs the kernel of paged_decode_attn, the keys of each
- * (sequence, KV head) split over the SMs; longer chunks run per query tile.
+ * (sequence, KV head) split over the SMs; longer chunks run per query tile, whose keys are
+ * split when the tiles are few.
  *
  *   q_chunk, k_cache, v_cache, kv_off, prefix_len   as for sparse_chunk_attn: the chunk's
  *               own rows have been written (rows prefix_len[b] .. + chunk - 1)
@@ -381,7 +382,8 @@ quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, co
                                int window, int n_sink, void* out, void* workspace, size_t ws_bytes,
                                void* stream);
 
-/* Bytes of device scratch window_chunk_attn() needs (0 unless chunk = 1; 0 if invalid). */
+/* Bytes of device scratch window_chunk_attn() needs (0 if the arguments are invalid; 0 for
+ * fp32 chunks, and for bf16 chunks of enough query tiles to fill the GPU). */
 size_t window_chunk_attn_workspace_size(const quoka_shape* shape, int max_prefix, int window);
 
 /*

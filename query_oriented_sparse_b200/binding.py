@@ -413,7 +413,7 @@ def window_chunk_attn(q_chunk: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
             out = torch.empty_like(q_chunk)
         else:
             _need("out", out, q_chunk.shape, dt, dev)
-        n = window_workspace_size(shape, max(prefix_len), window) if shape.chunk == 1 else 0
+        n = window_workspace_size(shape, max(prefix_len), window) if workspace is None else 0
         workspace, ws_bytes = _scratch(workspace, n, dev)
         _check(lib().window_chunk_attn(
             ctypes.byref(shape), _ptr(q_chunk), _ptr(k_cache), _ptr(v_cache), _host_i64(kv_off),

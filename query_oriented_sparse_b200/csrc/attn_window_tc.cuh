@@ -1,362 +1,685 @@
-// Window attention on tensor cores on one SM (bf16, d = 64): attn_window_tc2.cuh's work on
-// attn_tc.cuh's pipeline (two 128-row query tiles per CTA, one per softmax half, 128-row
-// tcgen05 MMAs).  The blocks, the masks and the cleaning of V tiles are those of
-// attn_window_tc2.cuh; the warps of query tile 0 clean for both, whose P.V come after theirs.
+// Window attention on tensor cores (bf16): the chunk's queries over a sliding window of the
+// contiguous cache and a few first tokens; out = softmax(q . k^T / sqrt(d)) . v over the keys
+// j <= p with j < n_sink or j > p - window, p the query's position.
+//
+// A tile is a run of positions of one (sequence, KV head): 128 rows per SM pack the G query
+// heads of the KV head at TP = 128 / G positions each.  d = 128 runs on SM pairs (clusters of
+// two CTAs, 2 TP positions, 256-row tcgen05 MMAs with cta_group::2, each SM holding half of
+// every K and V block), d = 64 on single SMs, whose K and V blocks are half the size.  K and V
+// come straight from the cache by TMA: the keys of a tile are one run of rows after the first
+// tokens, and blocks of 128 keys start at the oldest key that the tile's first position sees,
+// so a tile walks the fewest blocks.  Tiles of neighbouring positions run at the same time and
+// share most of their keys in L2.
+//
+// What bounds it is the chain S = Q K^T -> softmax -> O += P V of each tile: tensor cores and
+// exponentials take about the same time, and windows make tiles short, so starting and
+// finishing a tile weighs as much as ten blocks.  So every cluster runs two tiles at once, each
+// with its own loader warp, MMA thread, eight softmax warps, S and O in TMEM (S_x at columns
+// 128 x, P over it; O_x at 256 + 128 x), Q buffer and rings of two K and two V stages, and the two never
+// wait for each other: one tile's start, end and masked blocks pass under the other's work.
+// The clusters resident at once walk the tile list, cluster c taking tiles c, c + N, ...,
+// its two streams in turn.
+//
+// Softmax: one thread per row and 64-key half of a block; the halves agree on the block's
+// maximum through shared memory.  The running maximum and sum are fp32; O is rescaled in TMEM
+// only when the maximum grows by more than 2^8.  P is rounded to bf16 for its MMA (the row sum
+// is taken from the unrounded weights).
+//
+// A block that not every row sees whole (the diagonal, the window's lower edge, the end of the
+// first tokens) is masked by selection.  Its V tile is searched first for values that are not
+// finite, in rows that nobody may see (another sequence's, or memory never written) or that
+// some queries of the tile see: they are replaced by zero in shared memory and mark the tile,
+// and the epilogue adds them to the rows that do see them.  Without this 0 * NaN would carry
+// a masked row into every query of the tile.
+//
+// When the tiles are fewer than the streams (short chunks), each tile's blocks are split over
+// several units, which leave unnormalised partials (fp32) for the join kernel.
+//
+// Every mbarrier wait is bounded; the only unbounded waits are the cluster barriers and the
+// named barriers of a row's two halves, which every thread reaches on every path.
 #pragma once
-#include "attn_tc.cuh"
-#include "attn_window_tc2.cuh"
+#include <cooperative_groups.h>
+#include "attn_tc2.cuh"
+#include "attn_window.cuh"
 
 namespace quoka {
 
-__global__ void __launch_bounds__(ATC_THREADS, 1)
+constexpr int AWT_THREADS = 640;   // warps 0-1 load, 2-3 MMA, 4-11 and 12-19 softmax
+constexpr int AWT_ST = 2;          // K stages, and V stages, per stream
+constexpr int AWT_BK = 128;        // keys per block
+
+template <int D>
+struct AwtCfg {
+  static constexpr bool PAIR = D == 128;
+  static constexpr int CTAS = PAIR ? 2 : 1;        // CTAs per cluster
+  static constexpr int KB = D / 64;
+  static constexpr int Q_BYTES = 128 * D * 2;      // a CTA's query tile
+  static constexpr int H_BYTES = 16384;            // a CTA's share of a K or V block
+  static constexpr int STREAM = Q_BYTES + 2 * AWT_ST * H_BYTES;
+  static constexpr int BARS = 4 + 5 * AWT_ST;      // per stream
+  static constexpr int XBUF = 2 * 2 * 2 * 128 * 4; // [stream][slot set][half][row]
+  static constexpr int SMEM = 1024 + 2 * STREAM + 2 * BARS * 8 + 16 + 16 + XBUF;
+};
+
+struct WindowTcParams {
+  int h_q, h_kv, G, C, TP, window, n_sink;
+  int nsplit;                      // units per tile
+  long long rows_per_head;
+  float scale_log2;                // log2(e) / sqrt(d)
+  float* part;                     // [tile][unit][rows of the cluster][D], then
+  float* part_ml;                  // [tile][unit][rows of the cluster][2], when nsplit > 1
+};
+
+// A unit of work: blocks [j0, j1) of the nblk blocks of a tile.
+struct WindowUnit {
+  int b, g, t0;
+  int p_lo, p_hi;                  // absolute positions of the tile's first and last query
+  int ns, w0, nsb;                 // first tokens [0, ns) in nsb blocks, then keys w0 .. p_hi
+  int j0, j1;
+  long long row0;                  // cache row of the sequence's position 0
+
+  __device__ __forceinline__ int start(int j) const { return j < nsb ? j * AWT_BK : w0 + (j - nsb) * AWT_BK; }
+  __device__ __forceinline__ int end(int j) const { return j < nsb ? ns : p_hi + 1; }
+  // every query of the tile sees every key of block j
+  __device__ __forceinline__ bool whole(int j, int window, int n_sink) const {
+    const int k0 = start(j);
+    return k0 + AWT_BK <= end(j) && k0 + AWT_BK - 1 <= p_lo && (k0 > p_hi - window || k0 + AWT_BK <= n_sink);
+  }
+};
+
+__device__ __forceinline__ WindowUnit window_unit(const WindowTcParams& p, const SeqTable& tab, int unit, int ntp,
+                                                  int span) {
+  WindowUnit u;
+  const unsigned tile = (unsigned)unit / (unsigned)p.nsplit, rest = tile / (unsigned)ntp;
+  u.t0 = (ntp - 1 - (int)(tile - rest * ntp)) * span;      // longest key ranges first
+  u.b = (int)(rest / (unsigned)p.h_kv);
+  u.g = (int)rest - u.b * p.h_kv;
+  const int P = tab.prefix[u.b];
+  u.p_lo = P + u.t0;
+  u.p_hi = P + min(p.C, u.t0 + span) - 1;
+  const WindowSpan s = window_span(u.p_lo, u.p_hi, p.window, p.n_sink);
+  u.ns = s.ns;
+  u.w0 = s.w0;
+  u.nsb = (s.ns + AWT_BK - 1) / AWT_BK;
+  const int nblk = u.nsb + (s.p1 - s.w0) / AWT_BK + 1;
+  const unsigned sp = (unsigned)unit - tile * p.nsplit;    // nblk < 2^24 and nsplit <= 32
+  u.j0 = (int)(nblk * sp / (unsigned)p.nsplit);
+  u.j1 = (int)(nblk * (sp + 1) / (unsigned)p.nsplit);
+  u.row0 = (long long)u.g * p.rows_per_head + tab.kv_off[u.b];
+  return u;
+}
+
+// Replaces by zero the values that are not finite in a thread's share of a V tile of 16 KB in
+// shared memory (thread tg of 256: the 16-byte vectors tg, tg + 256, ...).  Returns whether
+// there were any.
+__device__ __forceinline__ bool window_clean_v(uint4* v, int tg) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {            // an exponent of ones carries into the sign's place
+    const uint4 x = v[i * 256 + tg];
+    any |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
+           ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
+  }
+  if (!(any & 0x80008000u)) return false;
+  for (int i = 0; i < 4; ++i) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(v + i * 256 + tg);
+    for (int k = 0; k < 4; ++k) {
+      if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
+      if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu;
+    }
+  }
+  return true;
+}
+
+// Adds the values of 16 columns of V that window_clean_v took out of the unit's blocks to one
+// row's output: an infinity or NaN times a positive weight is itself.
+__device__ __noinline__ void window_add_bad(float* o, const __nv_bfloat16* v, const WindowUnit& u, int pos, int window,
+                                            int n_sink, int D) {
+  for (int j = u.j0; j < u.j1; ++j) {
+    if (u.whole(j, window, n_sink)) continue;
+    const int k0 = u.start(j), k1 = min(min(k0 + AWT_BK, u.end(j)), pos + 1);
+    for (int kk = k0; kk < k1; ++kk) {
+      if (!(kk < n_sink || kk > pos - window)) continue;
+      for (int c = 0; c < 16; ++c) {
+        const float x = __bfloat162float(v[(u.row0 + kk) * D + c]);
+        if (!isfinite(x)) o[c] += x;
+      }
+    }
+  }
+}
+
+// v[i] of lane l (l = lane % 4) becomes v[l] of lane i, within each four lanes.
+__device__ __forceinline__ void window_transpose4(uint4 (&v)[4], int lane) {
+#pragma unroll
+  for (int o = 1; o < 4; o <<= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & o) continue;
+      uint4 send = up ? v[i] : v[i + o];
+      send.x = __shfl_xor_sync(0xffffffffu, send.x, o);
+      send.y = __shfl_xor_sync(0xffffffffu, send.y, o);
+      send.z = __shfl_xor_sync(0xffffffffu, send.z, o);
+      send.w = __shfl_xor_sync(0xffffffffu, send.w, o);
+      if (up) v[i] = send; else v[i + o] = send;
+    }
+  }
+}
+
+// The low n bits (n held to 0 .. 32).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+template <int D>
+__global__ void __cluster_dims__(D == 128 ? 2 : 1, 1, 1) __launch_bounds__(AWT_THREADS, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ SeqTable tab,
                  const __grid_constant__ WindowTcParams p, const __nv_bfloat16* __restrict__ v_cache,
                  __nv_bfloat16* __restrict__ out) {
-  constexpr int D = 64, BK = 128;
-  using Cfg = AtcCfg<D>;
-  constexpr int KB = Cfg::KB;
+  using Cfg = AwtCfg<D>;
+  constexpr bool PAIR = Cfg::PAIR;
+  namespace cg = cooperative_groups;
+  cg::cluster_group cluster = cg::this_cluster();
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = ptx::smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
-  uint8_t* sQ = smem;
-  uint8_t* sK = sQ + Cfg::Q_BYTES;
-  uint8_t* sV = sK + Cfg::K_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(sV + Cfg::V_BYTES);
-  uint64_t* qfull = bars;
-  uint64_t* kfull = bars + 1;
-  uint64_t* kempty = kfull + ATC_KST;
-  uint64_t* vfull = kempty + ATC_KST;
-  uint64_t* vempty = vfull + ATC_VST;
-  uint64_t* sfull = vempty + ATC_VST;   // [2]
-  uint64_t* pready = sfull + 2;         // [2]
-  uint64_t* odone = pready + 2;         // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odone + 2);
-  float* xbuf = reinterpret_cast<float*>(tmem_slot + 4);
-  volatile int* mark = reinterpret_cast<volatile int*>(xbuf + Cfg::XBUF / 4);   // a cleaned value was not finite
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.z, g = blockIdx.y;
-  const int npairs = (p.C + 2 * p.TP - 1) / (2 * p.TP);
-  const int pair = npairs - 1 - (int)blockIdx.x;           // longest key ranges first
-  const int t0 = pair * 2 * p.TP;
-  const WindowTile ti = window_tile(p, tab, b, g, t0, BK);
-  const int nblk = ti.nblk;
+  const uint32_t rank = PAIR ? cluster.block_rank() : 0u;
+  // this warp's stream, and that stream's memory
+  const int x = warp < 4 ? (warp & 1) : (warp - 4) >> 3;
+  uint8_t* sQ = smem + x * Cfg::STREAM;
+  uint8_t* sK = sQ + Cfg::Q_BYTES;
+  uint8_t* sV = sK + AWT_ST * Cfg::H_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + 2 * Cfg::STREAM) + x * Cfg::BARS;
+  uint64_t* qfull = bars;                  // this CTA's query tile landed
+  uint64_t* qpeer = bars + 1;              // (CTA 0) CTA 1's query tile landed
+  uint64_t* qempty = bars + 2;             // the S MMAs reading it are done (both CTAs)
+  uint64_t* pready = bars + 3;             // CTA 0: the pair's softmax warps of the stream wrote P
+  // [block parity], both CTAs: S of the block is done, and with it every MMA before; its K
+  // stage is free then
+  uint64_t* sfull = bars + 4;
+  uint64_t* vempty = sfull + AWT_ST;       // [stage], both CTAs: P.V of the block is done
+  uint64_t* kfull = vempty + AWT_ST;       // [stage], CTA 0: the K bytes of both CTAs
+  uint64_t* vfull = kfull + AWT_ST;        // [stage], this CTA's V bytes
+  uint64_t* vpeer = vfull + AWT_ST;        // [stage], CTA 0: CTA 1's V landed
+  uint64_t* end_bars = reinterpret_cast<uint64_t*>(smem + 2 * Cfg::STREAM) + 2 * Cfg::BARS;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(end_bars);
+  // [stream][unit parity] unit number + 1 when a value of one of its cleaned V blocks was not finite
+  volatile int* mark = reinterpret_cast<volatile int*>(tmem_slot + 4) + x * 2;
+  int* turn = reinterpret_cast<int*>(tmem_slot) + 1;       // 1 while an MMA thread issues
+  float* xbuf = reinterpret_cast<float*>(tmem_slot + 8);
 
-  if (threadIdx.x == 0) {
-    *mark = 0;
+  const int span = (PAIR ? 2 : 1) * p.TP;  // positions of a tile
+  const int ntp = (p.C + span - 1) / span;
+  const int units = ntp * p.h_kv * tab.batch * p.nsplit;
+  const int ncl = (int)gridDim.x / Cfg::CTAS, cid = (int)blockIdx.x / Cfg::CTAS;
+  // units of this cluster, and of this stream of it (the same for both CTAs)
+  const int cl_units = cid < units ? (units - 1 - cid) / ncl + 1 : 0;
+  const int my_units = (cl_units + 1 - x) >> 1;
+  constexpr uint16_t kBoth = 0x3;
+  auto unit_at = [&](int it) { return window_unit(p, tab, cid + (2 * it + x) * ncl, ntp, span); };
+  auto commit = [&](uint64_t* bar) {
+    if constexpr (PAIR) ptx::tc_commit_pair(bar, kBoth);
+    else ptx::tc_commit(bar);
+  };
+  // waits on a barrier that the other CTA of the pair arrives on
+  auto wait_pair = [&](uint64_t* bar, uint32_t parity) {
+    if constexpr (PAIR) return ptx::mbar_wait_cluster_sleep(bar, parity);
+    else return ptx::mbar_wait_sleep(bar, parity);
+  };
+
+  if (threadIdx.x < 64 && lane == 0) {     // warps 0 and 1: their streams' barriers
+    mark[0] = mark[1] = 0;
     ptx::mbar_init(qfull, 1);
-    for (int s = 0; s < ATC_KST; ++s) { ptx::mbar_init(&kfull[s], 1); ptx::mbar_init(&kempty[s], 1); }
-    for (int s = 0; s < ATC_VST; ++s) { ptx::mbar_init(&vfull[s], 1); ptx::mbar_init(&vempty[s], 1); }
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sfull[i], 1);
-      ptx::mbar_init(&pready[i], 8);
-      ptx::mbar_init(&odone[i], 1);
-    }
+    ptx::mbar_init(qpeer, 1);
+    ptx::mbar_init(qempty, 1);
+    ptx::mbar_init(pready, 8 * Cfg::CTAS);
+    for (int s = 0; s < 5 * AWT_ST; ++s) ptx::mbar_init(&sfull[s], 1);   // through vpeer
+    if (x == 0) *turn = 0;
     ptx::fence_mbar_init();
   }
-  if (warp == 1) {
-    ptx::tmem_alloc(tmem_slot, 512);
-    ptx::tmem_relinquish();
+  if (warp == 2) {
+    if constexpr (PAIR) {
+      ptx::tmem_alloc_pair(tmem_slot, 512);
+      ptx::tmem_relinquish_pair();
+    } else {
+      ptx::tmem_alloc(tmem_slot, 512);
+      ptx::tmem_relinquish();
+    }
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster.sync();      // barriers and TMEM of both CTAs ready
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0) {
-    // ---------------- loads: Q once by gather4, then K and V blocks by tiled TMA --------
+  if (warp < 2) {
+    // ---------------- loads ----------------
     if (lane == 0) {
       ptx::prefetch_tmap(&qmap);
       ptx::prefetch_tmap(&kmap);
       ptx::prefetch_tmap(&vmap);
     }
-    // Q: 2 tiles x 32 groups of 4 rows; row r of tile i is head r / TP, position
-    // t0 + i*TP + r % TP (rows past G*TP or C repeat a valid row; never stored)
-    if (lane == 0) ptx::mbar_expect_tx(qfull, (uint32_t)Cfg::Q_BYTES);
-    __syncwarp();
-    for (int grp = lane; grp < 64; grp += 32) {
-      const int tile = grp >> 5, r0 = (grp & 31) * 4;
-      int rows[4];
+    bool ok = true;
+    int jg = 0, uq = 0;                    // blocks, and units with blocks, so far
+    for (int it = 0; it < my_units && ok; ++it) {
+      const WindowUnit u = unit_at(it);
+      if (u.j0 == u.j1) continue;
+      for (int j = u.j0; j < u.j1 && ok; ++j, ++jg) {
+        const int st = jg % AWT_ST;
+        const uint32_t free = ((uint32_t)(jg / AWT_ST) & 1u) ^ 1u;   // the stage's block jg - AWT_ST
+        const int row = (int)u.row0 + u.start(j);
+        if (lane == 0) {
+          uint8_t* k_st = sK + st * Cfg::H_BYTES;
+          ok = ptx::mbar_wait_sleep(&sfull[st], free);
+          if (ok) {
+            if constexpr (PAIR) {
+              if (rank == 0) ptx::mbar_expect_tx(&kfull[st], 2u * Cfg::H_BYTES);
+              const uint32_t fbar = ptx::mapa_shared(ptx::smem_u32(&kfull[st]), 0);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = r0 + k;
-        int hl = r / p.TP, t = t0 + tile * p.TP + r % p.TP;
-        if (hl >= p.G || t >= p.C) { hl = 0; t = t0; }
-        rows[k] = (b * p.h_q + g * p.G + hl) * p.C + t;
+              for (int kb = 0; kb < 2; ++kb)
+                ptx::tma_load_2d_pair(k_st + kb * 8192, &kmap, fbar, kb * 64, row + 64 * (int)rank);
+            } else {
+              ptx::mbar_expect_tx(&kfull[st], (uint32_t)Cfg::H_BYTES);
+              ptx::tma_load_2d(k_st, &kmap, &kfull[st], 0, row);
+            }
+          }
+        }
+        if (j == u.j0) {
+          // Q: 32 groups of 4 rows; row r is head r / TP, position t0 + rank * TP + r % TP (rows
+          // past G * TP or C repeat a valid row; never stored)
+          if (lane == 0 && ok) ok = ptx::mbar_wait_sleep(qempty, ((uint32_t)uq & 1u) ^ 1u);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (lane == 0) ptx::mbar_expect_tx(qfull, (uint32_t)Cfg::Q_BYTES);
+          __syncwarp();
+          const int r0 = lane * 4;
+          int rows[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = r0 + k;
+            int hl = r / p.TP, t = u.t0 + (int)rank * p.TP + r % p.TP;
+            if (hl >= p.G || t >= p.C) { hl = 0; t = u.t0; }
+            rows[k] = (u.b * p.h_q + u.g * p.G + hl) * p.C + t;
+          }
+#pragma unroll
+          for (int kb = 0; kb < Cfg::KB; ++kb)
+            ptx::tma_gather4(sQ + kb * 16384 + r0 * 128, &qmap, qfull, kb * 64, rows[0], rows[1], rows[2], rows[3]);
+        }
+        if (lane == 0 && ok) {
+          ok = ptx::mbar_wait_sleep(&vempty[st], free);
+          if (ok) {
+            ptx::mbar_expect_tx(&vfull[st], (uint32_t)Cfg::H_BYTES);
+            ptx::tma_load_2d(sV + st * Cfg::H_BYTES, &vmap, &vfull[st], 64 * (int)rank, row);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
       }
-#pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-        ptx::tma_gather4(sQ + tile * Cfg::TILE_BYTES + kb * 16384 + r0 * 128, &qmap, qfull, kb * 64,
-                         rows[0], rows[1], rows[2], rows[3]);
+      ++uq;
     }
-    if (lane == 0) {
+  } else if (warp < 4) {
+    if (PAIR && rank == 1 && lane == 0) {
+      // ---------------- CTA 1: tell CTA 0 when this CTA's query tiles and V blocks landed ----------------
+      const uint32_t qpeer_c0 = ptx::mapa_shared(ptx::smem_u32(qpeer), 0);
+      const uint32_t vpeer_c0 = ptx::mapa_shared(ptx::smem_u32(vpeer), 0);
       bool ok = true;
-      for (int j = 0; j < nblk && ok; ++j) {
-        const int ks = j % ATC_KST, vs = j % ATC_VST;
-        const uint32_t kph = (uint32_t)(j / ATC_KST) & 1u, vph = (uint32_t)(j / ATC_VST) & 1u;
-        const int row = (int)ti.row0 + ti.start(j, BK);
-        ok = ptx::mbar_wait(&kempty[ks], kph ^ 1u);
+      int jg = 0, uq = 0;
+      for (int it = 0; it < my_units && ok; ++it) {
+        const WindowUnit u = unit_at(it);
+        if (u.j0 == u.j1) continue;
+        ok = ptx::mbar_wait_sleep(qfull, (uint32_t)uq & 1u);
         if (!ok) break;
-        ptx::mbar_expect_tx(&kfull[ks], (uint32_t)Cfg::TILE_BYTES);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          ptx::tma_load_2d(sK + ks * Cfg::TILE_BYTES + kb * 16384, &kmap, &kfull[ks], kb * 64, row);
-        ok = ptx::mbar_wait(&vempty[vs], vph ^ 1u);
-        if (!ok) break;
-        ptx::mbar_expect_tx(&vfull[vs], (uint32_t)Cfg::TILE_BYTES);
-#pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
-          ptx::tma_load_2d(sV + vs * Cfg::TILE_BYTES + kb * 16384, &vmap, &vfull[vs], kb * 64, row);
+        ptx::mbar_arrive_cluster(qpeer_c0);
+        ++uq;
+        for (int j = u.j0; j < u.j1 && ok; ++j, ++jg) {
+          ok = ptx::mbar_wait_sleep(&vfull[jg % AWT_ST], (uint32_t)(jg / AWT_ST) & 1u);
+          if (ok) ptx::mbar_arrive_cluster(vpeer_c0 + (uint32_t)(jg % AWT_ST) * 8u);
+        }
       }
     }
-  } else if (warp == 1) {
-    // ---------------- MMA issuer ----------------
-    if (lane == 0) {
-      const uint32_t idesc_s = ptx::idesc_bf16(128, 128, false);
-      const uint32_t idesc_o = ptx::idesc_bf16(128, D, true);
-      bool ok = ptx::mbar_wait(qfull, 0);
-      // Descriptor halves: only the start-address field (low half, address >> 4) moves as
-      // the MMAs step through k, the tile and the ring stage.
+    if (rank == 0 && lane == 0) {
+      // ---------------- MMA issuer: one thread per stream (of CTA 0 for the pair) ----------------
+      const uint32_t idesc_s = ptx::idesc_bf16(PAIR ? 256 : 128, AWT_BK, false);
+      const uint32_t idesc_o = ptx::idesc_bf16(PAIR ? 256 : 128, D, true);
       const uint64_t q_d = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
       const uint64_t k_d = ptx::sdesc_sw128(ptx::smem_u32(sK), 16, 1024);
       const uint64_t v_d = ptx::sdesc_sw128(ptx::smem_u32(sV), 16384, 1024);
       const uint32_t q_lo = (uint32_t)q_d, q_hi = (uint32_t)(q_d >> 32);
       const uint32_t k_lo = (uint32_t)k_d, k_hi = (uint32_t)(k_d >> 32);
       const uint32_t v_lo = (uint32_t)v_d, v_hi = (uint32_t)(v_d >> 32);
-      constexpr uint32_t TILE16 = (uint32_t)Cfg::TILE_BYTES >> 4;
-      auto issue_s = [&](int i, int j) {
-        const uint32_t a0 = q_lo + (uint32_t)i * TILE16;
-        const uint32_t b0 = k_lo + (uint32_t)(j % ATC_KST) * TILE16;
-        const uint32_t d = tmem + (uint32_t)(i * 128);
+      const uint32_t s_t = tmem + (uint32_t)(x * 128), o_t = tmem + 256u + (uint32_t)(x * 128);
+      auto s_mmas = [&](int jj) {
+        const uint32_t b0 = k_lo + (uint32_t)((jj % AWT_ST) * (Cfg::H_BYTES >> 4));
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb)
+        for (int kb = 0; kb < Cfg::KB; ++kb)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            ptx::mma_bf16_ss_lh(d, a0 + (uint32_t)(kb * 1024 + k * 2), q_hi, b0 + (uint32_t)(kb * 1024 + k * 2),
-                                k_hi, idesc_s, (kb | k) ? 1u : 0u);
-        ptx::tc_commit(&sfull[i]);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t a = q_lo + (uint32_t)(kb * 1024 + k * 2);
+            const uint32_t bb = b0 + (uint32_t)(kb * 512 + k * 2);
+            if constexpr (PAIR) ptx::mma_bf16_ss_pair(s_t, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
+            else ptx::mma_bf16_ss_lh(s_t, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
+          }
       };
-      auto issue_pv = [&](int i, int j) {
-        const uint32_t b0 = v_lo + (uint32_t)(j % ATC_VST) * TILE16;
-        const uint32_t d = tmem + (uint32_t)(256 + i * 128), pa = tmem + (uint32_t)(i * 128);
-        const uint32_t acc0 = j > 0 ? 1u : 0u;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)                          // 16 keys per MMA
-          ptx::mma_bf16_ts_lh(d, pa + (uint32_t)(k < 4 ? k * 8 : 96 + (k - 4) * 8), b0 + (uint32_t)(k * 128),
-                              v_hi, idesc_o, k > 0 ? 1u : acc0);
-        ptx::tc_commit(&odone[i]);
+      auto k_landed = [&](int jj) { return wait_pair(&kfull[jj % AWT_ST], (uint32_t)(jj / AWT_ST) & 1u); };
+      auto v_landed = [&](int jj) {
+        const uint32_t ph = (uint32_t)(jj / AWT_ST) & 1u;
+        return ptx::mbar_wait_sleep(&vfull[jj % AWT_ST], ph) &&
+               (!PAIR || ptx::mbar_wait_cluster_sleep(&vpeer[jj % AWT_ST], ph));
       };
-      if (ok) ok = ptx::mbar_wait(&kfull[0], 0);
-      if (ok) {
-        ptx::tc_fence_after();
-        issue_s(0, 0);
-        issue_s(1, 0);
-        ptx::tc_commit(&kempty[0]);
-      }
-      for (int j = 0; j < nblk && ok; ++j) {
-        const uint32_t par = (uint32_t)j & 1u;
-        ok = ptx::mbar_wait(&vfull[j % ATC_VST], (uint32_t)(j / ATC_VST) & 1u);
-        if (ok) ok = ptx::mbar_wait(&pready[0], par);
+      // The two threads issue a block's MMAs in one run each, by turns.  Interleaved in the tensor
+      // pipe, both streams would wait for both runs, and their softmax then run at the same time.
+      auto take = [&]() -> bool {
+        if (atomicExch(turn, 1) == 0) return true;
+        const uint64_t t0 = ptx::globaltimer();
+        for (uint32_t i = 1; atomicExch(turn, 1) != 0; ++i)
+          if ((i & 255u) == 0 && ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
+            flag_error(ERR_WAIT_TIMEOUT);
+            return false;
+          }
+        return true;
+      };
+      auto give = [&]() { *reinterpret_cast<volatile int*>(turn) = 0; };
+      bool ok = true;
+      int jg = 0, uq = 0;
+      for (int it = 0; it < my_units && ok; ++it) {
+        const WindowUnit u = unit_at(it);
+        const int n = u.j1 - u.j0;
+        if (n == 0) continue;
+        ok = ptx::mbar_wait_sleep(qfull, (uint32_t)uq & 1u);
+        if (PAIR && ok) ok = ptx::mbar_wait_cluster_sleep(qpeer, (uint32_t)uq & 1u);
+        if (ok) ok = k_landed(jg);
+        if (!ok) break;
+        ok = take();
         if (!ok) break;
         ptx::tc_fence_after();
-        issue_pv(0, j);
-        const bool more = j + 1 < nblk;
-        if (more) {
-          ok = ptx::mbar_wait(&kfull[(j + 1) % ATC_KST], (uint32_t)((j + 1) / ATC_KST) & 1u);
+        s_mmas(jg);
+        give();
+        commit(&sfull[jg % AWT_ST]);
+        if (n == 1) commit(qempty);
+        // every wait of a block comes before its MMAs, which are issued back to back
+        for (int j = 0; j < n && ok; ++j, ++jg) {
+          const bool more = j + 1 < n;
+          ok = v_landed(jg) && (!more || k_landed(jg + 1)) && wait_pair(pready, (uint32_t)jg & 1u);
+          if (ok) ok = take();
           if (!ok) break;
           ptx::tc_fence_after();
-          issue_s(0, j + 1);
+          // P: keys 0-63 in columns 0-31 of S, keys 64-127 in columns 96-127
+          const uint32_t b0 = v_lo + (uint32_t)((jg % AWT_ST) * (Cfg::H_BYTES >> 4));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const uint32_t a = s_t + (uint32_t)(k < 4 ? k * 8 : 96 + (k - 4) * 8);
+            const uint32_t acc = (j > 0 || k > 0) ? 1u : 0u;
+            if constexpr (PAIR) ptx::mma_bf16_ts_pair(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
+            else ptx::mma_bf16_ts_lh(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
+          }
+          if (more) s_mmas(jg + 1);        // over P: after P.V has read it (issued in order)
+          give();
+          if (more) commit(&sfull[(jg + 1) % AWT_ST]);
+          commit(&vempty[jg % AWT_ST]);
+          if (j + 2 == n) commit(qempty);  // the unit's last S: its query buffer is free
         }
-        ok = ptx::mbar_wait(&pready[1], par);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        issue_pv(1, j);
-        ptx::tc_commit(&vempty[j % ATC_VST]);
-        if (more) {
-          issue_s(1, j + 1);
-          ptx::tc_commit(&kempty[(j + 1) % ATC_KST]);
-        }
+        ++uq;
       }
     }
   } else {
-    // ---------------- softmax: warps 2-9 tile 0, warps 10-17 tile 1 ----------------
-    // Warp w serves TMEM lanes 32 * (w % 4) .. + 31 (one query row per thread) and key
-    // half (w - 2) / 4 % 2 of every block; the two warps of a row exchange block maxima
-    // (and at the end row sums) through shared memory under a 64-thread named barrier.
-    const int tile = (warp - 2) >> 3;
-    const int half = ((warp - 2) >> 2) & 1;
+    // ---------------- softmax ----------------
+    const int half = ((warp - 4) >> 2) & 1;                 // key half of each block
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;                      // row of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_off + (uint32_t)(tile * 128 + half * 64);
-    const uint32_t p_addr = tmem + lane_off + (uint32_t)(tile * 128 + half * 96);
-    constexpr int DH = D / 2;                               // O columns of this half
-    const uint32_t o_addr = tmem + lane_off + (uint32_t)(256 + tile * 128 + half * DH);
-    float* xslot = xbuf + tile * 128 + r;
-    const int bar_id = 1 + tile * 4 + quarter;
-    // half 0 posts v, half 1 combines it with its own and posts the result for half 0
+    constexpr int DH = D / 2;
+    const uint32_t s_addr = tmem + lane_off + (uint32_t)(x * 128 + half * 64);
+    const uint32_t p_addr = tmem + lane_off + (uint32_t)(x * 128 + half * 96);
+    const uint32_t o_addr = tmem + lane_off + 256u + (uint32_t)(x * 128 + half * DH);
+    const int bar_id = 1 + x * 4 + quarter;
+    const uint32_t pready_c0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(pready), 0) : 0u;
+    // the two halves of a row post their values and each combines both; slots alternate
+    // between two sets, so one barrier per exchange suffices
+    int xphase = 0;
     auto exchange = [&](float v, bool is_max) -> float {
-      if (half == 0) *xslot = v;
+      float* slot = xbuf + ((xphase & 1) * 2 + x) * 256 + r;
+      slot[half * 128] = v;
       ptx::named_bar(bar_id, 64);
-      float res = v;
-      if (half == 1) {
-        res = is_max ? fmaxf(v, *xslot) : v + *xslot;
-        *xslot = res;
-      }
-      ptx::named_bar(bar_id, 64);
-      if (half == 0) res = *xslot;
-      return res;
+      const float a0 = slot[0], a1 = slot[128];
+      ++xphase;
+      return is_max ? fmaxf(a0, a1) : a0 + a1;
     };
-    const int hl = r / p.TP;
-    const int t = t0 + tile * p.TP + r % p.TP;
-    const bool row_valid = hl < p.G && t < p.C;
-    const int pos = ti.p_lo + tile * p.TP + r % p.TP;       // this row's absolute position
-    float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    // Both warps of a row pair take part in exactly one exchange per block and one at
-    // the end, whatever happens, so the named barrier can never wait for a warp that left:
-    // after a failed (timed-out) wait a warp skips the work but keeps the exchanges.
-    for (int j = 0; j < nblk; ++j) {
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&sfull[tile], (uint32_t)j & 1u));
-      if (!ok) {
-        (void)exchange(0.f, true);
-        continue;
-      }
-      ptx::tc_fence_after();
-      float s[64];
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t u[32];
-        ptx::tmem_ld32(s_addr + (uint32_t)c, u);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[c + i] = __uint_as_float(u[i]);
-      }
-      ptx::tmem_ld_wait();
-      if (!ti.whole(j, BK, p.window, p.n_sink)) {
-        const int j0 = ti.start(j, BK), jend = ti.end(j);
-        const int k0 = j0 + half * 64;
-#pragma unroll
-        for (int c = 0; c < 64; ++c) {
-          const int kk = k0 + c;
-          if (!(kk < jend && kk <= pos && (kk < p.n_sink || kk > pos - p.window))) s[c] = -INFINITY;
+    int jg = 0;
+    // The two warps of a row take part in exactly one exchange per block and one at the end of
+    // each unit, whatever happens: after a failed (timed-out) wait a warp skips the work but
+    // keeps the exchanges.
+    for (int it = 0; it < my_units; ++it) {
+      const WindowUnit u = unit_at(it);
+      const int pos = u.p_lo + (int)rank * p.TP + r % p.TP; // this row's position
+      float m_run = -INFINITY, l_run = 0.f;
+      for (int j = u.j0; j < u.j1; ++j, ++jg) {
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&sfull[jg % AWT_ST], (uint32_t)(jg / AWT_ST) & 1u));
+        if (!ok) {
+          (void)exchange(0.f, true);
+          continue;
         }
-        if (tile == 0) {
-          ok = __all_sync(0xffffffffu, ptx::mbar_wait(&vfull[j % ATC_VST], (uint32_t)(j / ATC_VST) & 1u));
-          const int tg = (warp - 2) * 32 + lane;             // 256 threads, half a row of V each
-          uint4* vrow = reinterpret_cast<uint4*>(sV + (j % ATC_VST) * Cfg::TILE_BYTES + (tg >> 1) * 128 + (tg & 1) * 64);
-          if (ok && window_clean_v(vrow, j0 + (tg >> 1) < jend)) {
-            *mark = 1;
-            __threadfence_block();
-          }
-          ptx::fence_proxy_async_smem();
+        ptx::tc_fence_after();
+        float s[64];
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t w[32];
+          ptx::tmem_ld32(s_addr + (uint32_t)c, w);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) s[c + i] = __uint_as_float(w[i]);
         }
-      }
-      float mx;
-      {
-        float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
-#pragma unroll
-        for (int c = 4; c < 60; c += 8) {
-          m0 = ptx::max3(m0, s[c], s[c + 1]);
-          m1 = ptx::max3(m1, s[c + 2], s[c + 3]);
-          m2 = ptx::max3(m2, s[c + 4], s[c + 5]);
-          m3 = ptx::max3(m3, s[c + 6], s[c + 7]);
-        }
-        m0 = ptx::max3(m0, s[60], s[61]);
-        m1 = ptx::max3(m1, s[62], s[63]);
-        mx = exchange(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), true);
-      }
-      const float m_cand = mx * p.scale_log2;
-      const bool grow = m_cand > m_run + ATC_RESCALE_LOG2 || (m_run == -INFINITY && m_cand > -INFINITY);
-      float alpha = 1.f;
-      if (grow) {
-        alpha = (m_run == -INFINITY) ? 0.f : ptx::ex2_approx(m_run - m_cand);
-        m_run = m_cand;
-        l_run *= alpha;
-      }
-      const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
-      float ls[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 64; c += 32) {
-        uint32_t pk[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float p0 = ptx::ex2_approx(fmaf(s[c + 2 * i], p.scale_log2, -m_use));
-          const float p1 = ptx::ex2_approx(fmaf(s[c + 2 * i + 1], p.scale_log2, -m_use));
-          ls[i & 3] += p0 + p1;
-          pk[i] = pack_bf16(p0, p1);
-        }
-        ptx::tmem_st16(p_addr + (uint32_t)(c / 2), pk);
-      }
-      l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-      if (ok && j > 0 && __any_sync(0xffffffffu, grow)) {
-        // O holds blocks 0..j-1 once the previous P.V of this tile has finished
-        ok = __all_sync(0xffffffffu, ptx::mbar_wait(&odone[tile], (uint32_t)(j - 1) & 1u));
-        if (ok) ptx::tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < (ok ? DH : 0); c += 16) {
-          uint32_t u[16];
-          ptx::tmem_ld16(o_addr + (uint32_t)c, u);
-          ptx::tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * alpha);
-          ptx::tmem_st16(o_addr + (uint32_t)c, u);
-        }
-      }
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (ok && lane == 0) ptx::mbar_arrive(&pready[tile]);
-    }
-    // epilogue: O / l -> bf16 rows of out[b, g*G + hl, t, :], this half's columns
-    if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(&odone[tile], (uint32_t)(nblk - 1) & 1u));
-    const float l_row = exchange(ok ? l_run : 0.f, false);   // every pair member reaches this
-    if (ok) {
-      ptx::tc_fence_after();
-      const float inv_l = 1.f / l_row;                        // every row sees at least its own key
-      const bool dirty = *mark != 0;
-      __nv_bfloat16* orow = out + ((size_t)(b * p.h_q + g * p.G + (row_valid ? hl : 0)) * p.C +
-                                   (row_valid ? t : 0)) * D + half * DH;
-#pragma unroll
-      for (int c = 0; c < DH; c += 16) {
-        uint32_t u[16];
-        ptx::tmem_ld16(o_addr + (uint32_t)c, u);
         ptx::tmem_ld_wait();
-        float o[16];
+        const bool whole = u.whole(j, p.window, p.n_sink);
+        if (!whole) {
+          const int k0 = u.start(j), kend = u.end(j);
+          // bits of this row and half: below min(kend, pos + 1), and at pos - window + 1 or
+          // later or below n_sink
+          const int b0 = k0 + half * 64;
+          const int hi = min(kend, pos + 1) - b0, lo = pos - p.window + 1 - b0, sk = p.n_sink - b0;
+          const uint32_t w0 = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
+          const uint32_t w1 = low_bits(hi - 32) & (~low_bits(lo - 32) | low_bits(sk - 32));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(u[i]) * inv_l;
-        if (dirty && row_valid) {
-          float x[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) x[i] = o[i];
-          window_add_bad(x, v_cache + half * DH + c, ti, BK, pos, p.window, p.n_sink, D);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = x[i];
+          for (int c = 0; c < 64; ++c)
+            if (!(((c < 32 ? w0 : w1) >> (c & 31)) & 1u)) s[c] = -INFINITY;
+          // clean this CTA's share of the V tile before P.V reads it (the stream's 256 threads)
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&vfull[jg % AWT_ST], (uint32_t)(jg / AWT_ST) & 1u));
+          const int tg = ((warp - 4) & 7) * 32 + lane;
+          if (ok && window_clean_v(reinterpret_cast<uint4*>(sV + (jg % AWT_ST) * Cfg::H_BYTES), tg)) {
+            mark[it & 1] = it + 1;
+            if constexpr (PAIR) {          // this CTA's columns are in the other's rows too
+              const uint32_t far = ptx::mapa_shared(ptx::smem_u32(const_cast<int*>(mark + (it & 1))), rank ^ 1u);
+              asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(far), "r"(it + 1) : "memory");
+            }
+            __threadfence();               // with the (relaxed) arrival below: a release of these stores
+            ptx::fence_proxy_async_smem();
+          }
         }
-        uint4 w0, w1;
-        w0.x = pack_bf16(o[0], o[1]);
-        w0.y = pack_bf16(o[2], o[3]);
-        w0.z = pack_bf16(o[4], o[5]);
-        w0.w = pack_bf16(o[6], o[7]);
-        w1.x = pack_bf16(o[8], o[9]);
-        w1.y = pack_bf16(o[10], o[11]);
-        w1.z = pack_bf16(o[12], o[13]);
-        w1.w = pack_bf16(o[14], o[15]);
-        if (row_valid) {
-          reinterpret_cast<uint4*>(orow + c)[0] = w0;
-          reinterpret_cast<uint4*>(orow + c)[1] = w1;
+        float mx;
+        {
+          float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+          for (int c = 4; c < 60; c += 8) {
+            m0 = ptx::max3(m0, s[c], s[c + 1]);
+            m1 = ptx::max3(m1, s[c + 2], s[c + 3]);
+            m2 = ptx::max3(m2, s[c + 4], s[c + 5]);
+            m3 = ptx::max3(m3, s[c + 6], s[c + 7]);
+          }
+          m0 = ptx::max3(m0, s[60], s[61]);
+          m1 = ptx::max3(m1, s[62], s[63]);
+          mx = exchange(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), true);
         }
+        const float m_cand = mx * p.scale_log2;
+        const bool grow = m_cand > m_run + AT2_RESCALE_LOG2 || (m_run == -INFINITY && m_cand > -INFINITY);
+        float alpha = 1.f;
+        if (grow) {
+          alpha = (m_run == -INFINITY) ? 0.f : ptx::ex2_approx(m_run - m_cand);
+          m_run = m_cand;
+          l_run *= alpha;
+        }
+        const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
+        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 64; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float p0 = ptx::ex2_approx(fmaf(s[c + 2 * i], p.scale_log2, -m_use));
+            const float p1 = ptx::ex2_approx(fmaf(s[c + 2 * i + 1], p.scale_log2, -m_use));
+            ls[i & 3] += p0 + p1;
+            pk[i] = pack_bf16x2(p0, p1);
+          }
+          ptx::tmem_st16(p_addr + (uint32_t)(c / 2), pk);
+        }
+        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        if (j > u.j0 && __any_sync(0xffffffffu, grow)) {
+          // O holds the unit's earlier blocks: S(j), which this warp has seen, was issued after
+          // their P.V, and its commit covers them
+#pragma unroll
+          for (int c = 0; c < DH; c += 16) {
+            uint32_t w[16];
+            ptx::tmem_ld16(o_addr + (uint32_t)c, w);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(__uint_as_float(w[i]) * alpha);
+            ptx::tmem_st16(o_addr + (uint32_t)c, w);
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        // relaxed arrive: P and the rescaled O are TMEM stores already completed by
+        // tcgen05.wait::st and ordered by the fence above; a release would stall the warp on
+        // unrelated memory operations (the stores of the unit before)
+        if (ok && lane == 0) {
+          if constexpr (PAIR) ptx::mbar_arrive_cluster_relaxed(pready_c0);
+          else ptx::mbar_arrive(pready);
+        }
+      }
+      // epilogue: O is final once the unit's last P.V has released its stage (that commit covers
+      // every earlier MMA; the stage's next release needs this warp's next P)
+      if (ok && u.j1 > u.j0)
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&vempty[(jg - 1) % AWT_ST], (uint32_t)((jg - 1) / AWT_ST) & 1u));
+      const float l_row = exchange(ok ? l_run : 0.f, false);   // every pair member reaches this
+      if (ok) {
+        ptx::tc_fence_after();
+        const bool dirty = mark[it & 1] == it + 1;
+        const bool split = p.nsplit > 1;
+        // split units leave O and (m, l); others every row's O / l (each sees its own key)
+        const float inv_l = split ? 1.f : 1.f / l_row;
+        const int hl = r / p.TP;
+        const int t = u.t0 + (int)rank * p.TP + r % p.TP;
+        const size_t prow = ((size_t)(cid + (2 * it + x) * ncl) * Cfg::CTAS + rank) * 128 + r;
+        if (split && half == 0) {
+          p.part_ml[prow * 2] = m_run;
+          p.part_ml[prow * 2 + 1] = l_row;
+        }
+        // output row of this thread, -1 for none
+        const int orow = hl < p.G && t < p.C ? (u.b * p.h_q + u.g * p.G + hl) * p.C + t : -1;
+#pragma unroll
+        for (int c = 0; c < (u.j1 > u.j0 ? DH : 0); c += 32) {
+          uint4 w4[4];                     // 32 output columns as bf16
+#pragma unroll
+          for (int cc = 0; cc < 32; cc += 16) {
+            uint32_t w[16];
+            ptx::tmem_ld16(o_addr + (uint32_t)(c + cc), w);
+            ptx::tmem_ld_wait();
+            float o[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[i]) * inv_l;
+            if (dirty && orow >= 0) {
+              float y[16];                 // (its address is taken here alone: o stays in registers)
+#pragma unroll
+              for (int i = 0; i < 16; ++i) y[i] = o[i];
+              window_add_bad(y, v_cache + half * DH + c + cc, u, pos, p.window, p.n_sink, D);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = y[i];
+            }
+            if (split) {
+              float4* d4 = reinterpret_cast<float4*>(p.part + prow * D + half * DH + c + cc);
+              if (orow >= 0) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d4[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint4& y = w4[cc / 8 + i];
+              y.x = pack_bf16x2(o[8 * i], o[8 * i + 1]);
+              y.y = pack_bf16x2(o[8 * i + 2], o[8 * i + 3]);
+              y.z = pack_bf16x2(o[8 * i + 4], o[8 * i + 5]);
+              y.w = pack_bf16x2(o[8 * i + 6], o[8 * i + 7]);
+            }
+          }
+          if (!split) {
+            // four lanes exchange their rows' vectors, so that each store writes 64 bytes of a row
+            window_transpose4(w4, lane);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int row = __shfl_sync(0xffffffffu, orow, (lane & ~3) + i);
+              if (row >= 0)
+                reinterpret_cast<uint4*>(out + (size_t)row * D + half * DH + c)[lane & 3] = w4[i];
+            }
+          }
+        }
+        ptx::tc_fence_before();
       }
     }
   }
 
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if constexpr (PAIR) cluster.sync();      // the pair's MMAs and loads are over on both SMs
+  if (warp == 2) {
     __syncwarp();
     ptx::tc_fence_after();
-    ptx::tmem_dealloc(tmem, 512);
+    if constexpr (PAIR) ptx::tmem_dealloc_pair(tmem, 512);
+    else ptx::tmem_dealloc(tmem, 512);
   }
+}
+
+// Joins the units of each tile: out = sum_u O_u 2^(m_u - M) / sum_u l_u 2^(m_u - M).  One thread
+// per 8 output columns.
+constexpr int AWJ_THREADS = 256;
+template <int D>
+__global__ void __launch_bounds__(AWJ_THREADS)
+window_join_kernel(const __grid_constant__ WindowTcParams p, long long total, __nv_bfloat16* __restrict__ out) {
+  using Cfg = AwtCfg<D>;
+  constexpr int VPR = D / 8;
+  const long long e = (long long)blockIdx.x * AWJ_THREADS + threadIdx.x;
+  if (e >= total) return;
+  const long long row = e / VPR;           // (b * h_q + h) * C + t
+  const int c = (int)(e - row * VPR) * 8;
+  const int t = (int)(row % p.C);
+  const long long bh = row / p.C;
+  const int b = (int)(bh / p.h_q), h = (int)(bh - (long long)b * p.h_q);
+  const int g = h / p.G, hl = h - g * p.G;
+  const int span = Cfg::CTAS * p.TP, ntp = (p.C + span - 1) / span;
+  const int in = t % span, rank = in / p.TP;
+  const long long tile = ((long long)b * p.h_kv + g) * ntp + (ntp - 1 - t / span);
+  const size_t r0 = ((size_t)tile * p.nsplit * Cfg::CTAS + rank) * 128 + hl * p.TP + in % p.TP;
+  const size_t step = (size_t)Cfg::CTAS * 128;
+  float M = -INFINITY, L = 0.f, o[8];
+  for (int s = 0; s < p.nsplit; ++s)
+    if (p.part_ml[(r0 + s * step) * 2 + 1] != 0.f) M = fmaxf(M, p.part_ml[(r0 + s * step) * 2]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  for (int s = 0; s < p.nsplit; ++s) {
+    const float l = p.part_ml[(r0 + s * step) * 2 + 1];
+    if (l == 0.f) continue;                // no visible key: its O is not set
+    const float f = exp2f(p.part_ml[(r0 + s * step) * 2] - M);
+    L = fmaf(l, f, L);
+    const float4* src = reinterpret_cast<const float4*>(p.part + (r0 + s * step) * D + c);
+    const float4 a = src[0], d = src[1];
+    o[0] = fmaf(a.x, f, o[0]); o[1] = fmaf(a.y, f, o[1]); o[2] = fmaf(a.z, f, o[2]); o[3] = fmaf(a.w, f, o[3]);
+    o[4] = fmaf(d.x, f, o[4]); o[5] = fmaf(d.y, f, o[5]); o[6] = fmaf(d.z, f, o[6]); o[7] = fmaf(d.w, f, o[7]);
+  }
+  const float inv = 1.f / L;
+  uint4 w;
+  w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
+  w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
+  w.z = pack_bf16x2(o[4] * inv, o[5] * inv);
+  w.w = pack_bf16x2(o[6] * inv, o[7] * inv);
+  reinterpret_cast<uint4*>(out)[e] = w;
 }
 
 }  // namespace quoka

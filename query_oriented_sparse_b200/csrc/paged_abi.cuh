@@ -180,8 +180,37 @@ quoka_status launch_window_simt(const Dims& d, const SeqTable& tab, long long ro
   return QUOKA_OK;
 }
 
-// Clusters (SM pairs) of the window kernel that fit on the device at once.
-int window_resident_pairs(int smem) {
+// Units per tile of the tensor-core form and the space of their partials.
+constexpr int WINDOW_STREAMS_PAIR = 148;      // two streams on each of 74 SM pairs
+constexpr int WINDOW_STREAMS_SINGLE = 296;    // two on each of 148 SMs
+constexpr int WINDOW_MIN_BLOCKS = 4;          // 128-key blocks per unit at least
+constexpr int WINDOW_MAX_SPLIT = 32;
+
+struct WindowWs {
+  long long tiles;
+  int nsplit;
+  size_t part, part_ml, total;
+};
+
+WindowWs window_tc_ws(const Dims& d, int max_prefix, int window) {
+  WindowWs w;
+  const bool pair = d.D == 128;
+  const int ctas = pair ? 2 : 1, span = ctas * (128 / d.G);
+  w.tiles = (long long)((d.C + span - 1) / span) * d.h_kv * d.batch;
+  const long long blocks = (std::min<long long>(window, (long long)max_prefix + 1) + span + AWT_BK - 1) / AWT_BK;
+  const long long room = (pair ? WINDOW_STREAMS_PAIR : WINDOW_STREAMS_SINGLE) / w.tiles;
+  w.nsplit = (int)std::max<long long>(1, std::min(std::min(room, blocks / WINDOW_MIN_BLOCKS), (long long)WINDOW_MAX_SPLIT));
+  const size_t rows = w.nsplit > 1 ? (size_t)w.tiles * w.nsplit * ctas * 128 : 0;
+  w.part = 0;
+  w.part_ml = align_up(rows * d.D * 4, 256);
+  w.total = align_up(w.part_ml + rows * 8, 256);
+  return w;
+}
+
+// Clusters of the window kernel that fit on the device at once.
+template <int D>
+int window_resident(int smem) {
+  if (D != 128) return sm_count();
   static std::mutex mu;
   static std::map<int, int> cache;
   int dev = 0;
@@ -191,10 +220,10 @@ int window_resident_pairs(int smem) {
   if (it != cache.end()) return it->second;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * sm_count(), 1, 1);
-  cfg.blockDim = dim3(AT2_THREADS, 1, 1);
+  cfg.blockDim = dim3(AWT_THREADS, 1, 1);
   cfg.dynamicSmemBytes = (size_t)smem;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, (const void*)window_tc2_kernel, &cfg) != cudaSuccess || n <= 0) {
+  if (cudaOccupancyMaxActiveClusters(&n, (const void*)window_tc_kernel<D>, &cfg) != cudaSuccess || n <= 0) {
     (void)cudaGetLastError();
     n = sm_count() / 2;
   }
@@ -202,10 +231,11 @@ int window_resident_pairs(int smem) {
   return n;
 }
 
-// bf16: 128-row query tiles, the G heads of a KV head at 128 / G positions each, two to a tile.
 template <int D>
 quoka_status launch_window_tc(const Dims& d, const SeqTable& tab, long long rows, const void* q, const void* k,
-                              const void* v, int window, int n_sink, void* out, cudaStream_t st) {
+                              const void* v, int window, int n_sink, void* out, unsigned char* ws, const WindowWs& w,
+                              cudaStream_t st) {
+  using Cfg = AwtCfg<D>;
   WindowTcParams p;
   p.h_q = d.h_q;
   p.h_kv = d.h_kv;
@@ -214,34 +244,33 @@ quoka_status launch_window_tc(const Dims& d, const SeqTable& tab, long long rows
   p.TP = 128 / d.G;
   p.window = window;
   p.n_sink = n_sink;
+  p.nsplit = w.nsplit;
   p.rows_per_head = rows;
   p.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+  if (w.tiles * w.nsplit >= (1ll << 30)) return fail(QUOKA_ERR_UNSUPPORTED, "more than 2^30 query tiles");
   CUtensorMap qmap, kmap, vmap;
   quoka_status s;
   const uint64_t kv_rows = (uint64_t)d.h_kv * rows;
   if ((s = make_map_bf16(&qmap, q, (uint64_t)d.batch * d.h_q * d.C, D, 64, 1, "q_chunk")) != QUOKA_OK) return s;
-  if ((s = make_map_bf16(&kmap, k, kv_rows, D, 64, D == 128 ? 64 : 128, "k_cache")) != QUOKA_OK) return s;
-  if ((s = make_map_bf16(&vmap, v, kv_rows, D, 64, 128, "v_cache")) != QUOKA_OK) return s;
-  const int npairs = (d.C + 2 * p.TP - 1) / (2 * p.TP);
-  const long long tiles = (long long)npairs * d.h_kv * d.batch;
-  if (tiles >= (1ll << 31)) return fail(QUOKA_ERR_UNSUPPORTED, "more than 2^31 query tiles");
+  if ((s = make_map_bf16(&kmap, k, kv_rows, D, 64, AWT_BK / Cfg::CTAS, "k_cache")) != QUOKA_OK) return s;
+  if ((s = make_map_bf16(&vmap, v, kv_rows, D, 64, AWT_BK, "v_cache")) != QUOKA_OK) return s;
+  const int smem = Cfg::SMEM;
   cudaError_t e;
-  if constexpr (D == 128) {
-    const int smem = AwtCfg::SMEM;
-    if ((e = ensure_smem(window_tc2_kernel, smem)) != cudaSuccess) return cuda_fail(e, "window_tc2 smem");
-    const int ncl = (int)std::min<long long>(tiles, window_resident_pairs(smem));
-    window_tc2_kernel<<<dim3(2 * ncl), AT2_THREADS, smem, st>>>(qmap, kmap, vmap, tab, p,
-                                                                 reinterpret_cast<const __nv_bfloat16*>(v),
-                                                                 reinterpret_cast<__nv_bfloat16*>(out));
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_tc2 launch");
-    prof_mark(st, "window_tc2_kernel");
-  } else {
-    const int smem = AtcCfg<D>::SMEM + 16;
-    if ((e = ensure_smem(window_tc_kernel, smem)) != cudaSuccess) return cuda_fail(e, "window_tc smem");
-    window_tc_kernel<<<dim3(npairs, d.h_kv, d.batch), ATC_THREADS, smem, st>>>(
-        qmap, kmap, vmap, tab, p, reinterpret_cast<const __nv_bfloat16*>(v), reinterpret_cast<__nv_bfloat16*>(out));
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_tc launch");
-    prof_mark(st, "window_tc_kernel");
+  if ((e = ensure_smem(window_tc_kernel<D>, smem)) != cudaSuccess) return cuda_fail(e, "window_tc smem");
+  const int ncl = (int)std::min<long long>(w.tiles * w.nsplit, window_resident<D>(smem));
+  window_tc_kernel<D><<<Cfg::CTAS * ncl, AWT_THREADS, smem, st>>>(qmap, kmap, vmap, tab, p,
+                                                                  reinterpret_cast<const __nv_bfloat16*>(v),
+                                                                  reinterpret_cast<__nv_bfloat16*>(out));
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_tc launch");
+  prof_mark(st, "window_tc_kernel");
+  if (w.nsplit > 1) {
+    const long long total = (long long)d.batch * d.h_q * d.C * (D / 8);
+    window_join_kernel<D><<<(unsigned)((total + AWJ_THREADS - 1) / AWJ_THREADS), AWJ_THREADS, 0, st>>>(
+        p, total, reinterpret_cast<__nv_bfloat16*>(out));
+    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_join launch");
+    prof_mark(st, "window_join_kernel");
   }
   return QUOKA_OK;
 }
@@ -252,8 +281,9 @@ extern "C" {
 
 size_t window_chunk_attn_workspace_size(const quoka_shape* shape, int max_prefix, int window) {
   Dims d;
-  if (check_shape(shape, &d) != QUOKA_OK || max_prefix < 0 || window < 1 || d.C != 1) return 0;
-  return window_ws(d, max_prefix).total;
+  if (check_shape(shape, &d) != QUOKA_OK || max_prefix < 0 || window < 1) return 0;
+  if (d.C == 1) return window_ws(d, max_prefix).total;
+  return d.dt == QUOKA_BF16 ? window_tc_ws(d, max_prefix, window).total : 0;
 }
 
 quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, const void* k_cache,
@@ -293,8 +323,11 @@ quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, co
     if (d.dt == QUOKA_F32)
       return d.D == 64 ? launch_window_simt<float, 64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
                        : launch_window_simt<float, 128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
-    return d.D == 64 ? launch_window_tc<64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
-                     : launch_window_tc<128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
+    const WindowWs w = window_tc_ws(d, tab.max_prefix, window);
+    if ((s = check_ws(workspace, ws_bytes, w.total)) != QUOKA_OK) return s;
+    auto* ws = reinterpret_cast<unsigned char*>(workspace);
+    return d.D == 64 ? launch_window_tc<64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, ws, w, st)
+                     : launch_window_tc<128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, ws, w, st);
   });
 }
 

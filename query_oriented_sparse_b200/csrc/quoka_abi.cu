@@ -28,7 +28,6 @@
 #include "selcache.cuh"
 #include "perq_tc.cuh"
 #include "attn_window.cuh"
-#include "attn_window_tc2.cuh"
 #include "attn_window_tc.cuh"
 #include "attn_stream.cuh"
 

@@ -60,6 +60,12 @@ CASES = [
     (64, 1, 64, 9, (260,), 100, 1),
     (8, 2, 128, 2, (3000,), 2000, 4),             # a short chunk
     (4, 4, 128, 640, (640,), 640, 0),
+    (8, 2, 128, 16, (5000, 0, 600), 4000, 70),    # tiles split over their keys, some with fewer keys than units
+    (8, 2, 64, 16, (5000, 0, 600), 4000, 70),
+    (32, 8, 128, 2, (3000, 2999), 2500, 4),
+    (64, 1, 64, 3, (4000,), 100000, 0),
+    (1, 1, 128, 1000, (500,), 300, 4),            # more units than streams
+    (8, 8, 64, 3000, (0,), 200, 4),
 ]
 TOKEN_CASES = [
     (4, 1, 64, (0, 1, 40, 300), 37, 4),
@@ -185,6 +191,25 @@ def test_graph_replay_and_other_stream(cuda_device):
         assert torch.equal(out, Bd.window_chunk_attn(q, k, v, off, prefix, window, n_sink))
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_rows_in_split_tiles(d, cuda_device):
+    """As above with each tile's keys split over several units."""
+    prefix, window, n_sink, C = (2500,), 2000, 0, 12
+    q, k, v, off = make(8, 2, d, C, prefix, BF, seed=6)
+    assert Bd.window_workspace_size(Bd.make_shape(1, 8, 2, d, C, BF), 2500, window) > 0
+    clean = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), off, prefix, window, n_sink).cpu()
+    for at in (2500 + 7, 2500 - 1995, 2500 + 11):
+        v2 = v.clone()
+        v2[:, at, 11] = float("nan")
+        out = Bd.window_chunk_attn(q.cuda(), k.cuda(), v2.cuda(), off, prefix, window, n_sink).cpu()
+        p = 2500 + torch.arange(C)
+        sees = (at <= p) & (at > p - window)
+        assert 0 < int(sees.sum()) < C or at == 2500 + 11
+        assert torch.equal(out[0][:, ~sees], clean[0][:, ~sees])
+        assert out[0][:, sees, 11].isnan().all() and torch.isfinite(out[0][:, sees, :11].float()).all()
+
+
 # ---- refusals (host checks: no GPU needed, nothing is launched) --------------------------------
 
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
@@ -224,10 +249,15 @@ def test_rejects(case, status):
     assert Bd.lib().quoka_last_error().decode()
 
 
-def test_workspace_only_for_a_token():
+def test_workspace_size():
+    for C, dtype, window in ((1, BF, 100), (1, F32, 100), (16, BF, 4096)):
+        n = Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, C, dtype), 4096, window)
+        assert n > 0 and n % 256 == 0
+    # one unit per tile: short windows, many tiles, fp32
     assert Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, 64, BF), 4096, 100) == 0
-    n = Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, 1, BF), 4096, 100)
-    assert n > 0 and n % 256 == 0
+    assert Bd.window_workspace_size(Bd.make_shape(8, 32, 8, 128, 4096, BF), 4096, 4096) == 0
+    assert Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, 16, F32), 4096, 4096) == 0
+    assert Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 96, 16, BF), 4096, 4096) == 0
 
 
 def test_binding_refuses_strides_shapes_and_types():
