@@ -18,7 +18,8 @@
 // 128 x, P over it; O_x at 256 + 128 x), Q buffer and rings of two K and two V stages, and the two never
 // wait for each other: one tile's start, end and masked blocks pass under the other's work.
 // The clusters resident at once walk the tile list, cluster c taking tiles c, c + N, ...,
-// its two streams in turn.
+// its two streams in turn; the last of an odd number both streams share by key blocks, and
+// stream 1's half reaches stream 0 through shared memory.
 //
 // Softmax: one thread per row and 64-key half of a block; the halves agree on the block's
 // maximum through shared memory.  The running maximum and sum are fp32; O is rescaled in TMEM
@@ -32,7 +33,7 @@
 // and the epilogue adds them to the rows that do see them.  Without this 0 * NaN would carry
 // a masked row into every query of the tile.
 //
-// When the tiles are fewer than the streams (short chunks), each tile's blocks are split over
+// When the tiles are fewer than the clusters (short chunks), each tile's blocks are split over
 // several units, which leave unnormalised partials (fp32) for the join kernel.
 //
 // Every mbarrier wait is bounded; the only unbounded waits are the cluster barriers and the
@@ -57,8 +58,9 @@ struct AwtCfg {
   static constexpr int H_BYTES = 16384;            // a CTA's share of a K or V block
   static constexpr int STREAM = Q_BYTES + 2 * AWT_ST * H_BYTES;
   static constexpr int BARS = 4 + 5 * AWT_ST;      // per stream
-  static constexpr int XBUF = 2 * 2 * 2 * 128 * 4; // [stream][slot set][half][row]
-  static constexpr int SMEM = 1024 + 2 * STREAM + 2 * BARS * 8 + 16 + 16 + XBUF;
+  static constexpr int XBUF = 2 * 2 * 2 * 128 * 4; // [slot set][stream][half][row]
+  static constexpr int MBUF = 2 * 128 * 4;         // a shared unit's (m, l) of stream 1
+  static constexpr int SMEM = 1024 + 2 * STREAM + (2 * BARS + 1) * 8 + 8 + 16 + 16 + XBUF + MBUF;
 };
 
 struct WindowTcParams {
@@ -203,11 +205,15 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   uint64_t* vfull = kfull + AWT_ST;        // [stage], this CTA's V bytes
   uint64_t* vpeer = vfull + AWT_ST;        // [stage], CTA 0: CTA 1's V landed
   uint64_t* end_bars = reinterpret_cast<uint64_t*>(smem + 2 * Cfg::STREAM) + 2 * Cfg::BARS;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(end_bars);
+  uint64_t* merge = end_bars;              // stream 1's half of a shared unit lies in its rings
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(end_bars + 2);
   // [stream][unit parity] unit number + 1 when a value of one of its cleaned V blocks was not finite
   volatile int* mark = reinterpret_cast<volatile int*>(tmem_slot + 4) + x * 2;
   int* turn = reinterpret_cast<int*>(tmem_slot) + 1;       // 1 while an MMA thread issues
   float* xbuf = reinterpret_cast<float*>(tmem_slot + 8);
+  float* mbuf = xbuf + Cfg::XBUF / 4;      // [m, l][row]
+  // [column][row] of stream 1's O of a shared unit: over its K and V stages, which are done by then
+  float* obuf = reinterpret_cast<float*>(smem + Cfg::STREAM + Cfg::Q_BYTES);
 
   const int span = (PAIR ? 2 : 1) * p.TP;  // positions of a tile
   const int ntp = (p.C + span - 1) / span;
@@ -215,9 +221,18 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   const int ncl = (int)gridDim.x / Cfg::CTAS, cid = (int)blockIdx.x / Cfg::CTAS;
   // units of this cluster, and of this stream of it (the same for both CTAs)
   const int cl_units = cid < units ? (units - 1 - cid) / ncl + 1 : 0;
-  const int my_units = (cl_units + 1 - x) >> 1;
+  const int my_units = (cl_units + 1) >> 1;
   constexpr uint16_t kBoth = 0x3;
-  auto unit_at = [&](int it) { return window_unit(p, tab, cid + (2 * it + x) * ncl, ntp, span); };
+  // the streams take the cluster's units in turn, and share the blocks of the last of an odd number
+  auto shared_unit = [&](int it) { return 2 * it + 1 == cl_units; };
+  auto unit_at = [&](int it) {
+    const bool sh = shared_unit(it);
+    WindowUnit u = window_unit(p, tab, cid + (2 * it + (sh ? 0 : x)) * ncl, ntp, span);
+    const int mid = u.j0 + (u.j1 - u.j0 + 1) / 2;
+    if (sh && x == 0) u.j1 = mid;
+    if (sh && x == 1) u.j0 = mid;
+    return u;
+  };
   auto commit = [&](uint64_t* bar) {
     if constexpr (PAIR) ptx::tc_commit_pair(bar, kBoth);
     else ptx::tc_commit(bar);
@@ -235,7 +250,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     ptx::mbar_init(qempty, 1);
     ptx::mbar_init(pready, 8 * Cfg::CTAS);
     for (int s = 0; s < 5 * AWT_ST; ++s) ptx::mbar_init(&sfull[s], 1);   // through vpeer
-    if (x == 0) *turn = 0;
+    if (x == 0) {
+      *turn = 0;
+      ptx::mbar_init(merge, 8);
+    }
     ptx::fence_mbar_init();
   }
   if (warp == 2) {
@@ -560,21 +578,66 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       if (ok && u.j1 > u.j0)
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&vempty[(jg - 1) % AWT_ST], (uint32_t)((jg - 1) / AWT_ST) & 1u));
       const float l_row = exchange(ok ? l_run : 0.f, false);   // every pair member reaches this
+      const bool sh = shared_unit(it);
+      const bool dirty = mark[it & 1] == it + 1;
+      const int hl = r / p.TP;
+      const int t = u.t0 + (int)rank * p.TP + r % p.TP;
+      // output row of this thread, -1 for none
+      const int orow = hl < p.G && t < p.C ? (u.b * p.h_q + u.g * p.G + hl) * p.C + t : -1;
+      float l_all = l_row;
+      ptx::tc_fence_after();
+      if (sh && ok) {
+        // a shared unit: stream 1 leaves O, m and l, stream 0 joins them to its own
+        float* ob = obuf + half * DH * 128 + r;
+        if (x == 1) {
+          for (int c = 0; c < (u.j1 > u.j0 ? DH : 0); c += 16) {
+            uint32_t w[16];
+            ptx::tmem_ld16(o_addr + (uint32_t)c, w);
+            ptx::tmem_ld_wait();
+            float y[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(w[i]);
+            if (dirty && orow >= 0) window_add_bad(y, v_cache + half * DH + c, u, pos, p.window, p.n_sink, D);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) ob[(c + i) * 128] = y[i];
+          }
+          if (half == 0) {
+            mbuf[r] = m_run;
+            mbuf[128 + r] = l_row;
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(merge);
+          continue;                        // (the cluster's last unit)
+        }
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(merge, 0));
+        const float m1 = mbuf[r], l1 = ok ? mbuf[128 + r] : 0.f;
+        const float M = l1 != 0.f ? (l_row != 0.f ? fmaxf(m_run, m1) : m1) : m_run;
+        const float f0 = l_row != 0.f ? ptx::ex2_approx(m_run - M) : 0.f;
+        const float f1 = l1 != 0.f ? ptx::ex2_approx(m1 - M) : 0.f;
+        l_all = (l_row != 0.f ? l_row * f0 : 0.f) + (l1 != 0.f ? l1 * f1 : 0.f);
+        m_run = M;
+        for (int c = 0; c < (ok && u.j1 > u.j0 ? DH : 0); c += 16) {   // (stream 0 has blocks when stream 1 has)
+          uint32_t w[16];
+          ptx::tmem_ld16(o_addr + (uint32_t)c, w);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float a = f0 != 0.f ? __uint_as_float(w[i]) * f0 : 0.f;
+            w[i] = __float_as_uint(f1 != 0.f ? fmaf(ob[(c + i) * 128], f1, a) : a);
+          }
+          ptx::tmem_st16(o_addr + (uint32_t)c, w);
+        }
+        ptx::tmem_st_wait();
+      }
       if (ok) {
-        ptx::tc_fence_after();
-        const bool dirty = mark[it & 1] == it + 1;
         const bool split = p.nsplit > 1;
         // split units leave O and (m, l); others every row's O / l (each sees its own key)
-        const float inv_l = split ? 1.f : 1.f / l_row;
-        const int hl = r / p.TP;
-        const int t = u.t0 + (int)rank * p.TP + r % p.TP;
-        const size_t prow = ((size_t)(cid + (2 * it + x) * ncl) * Cfg::CTAS + rank) * 128 + r;
+        const float inv_l = split ? 1.f : 1.f / l_all;
+        const size_t prow = ((size_t)(cid + (2 * it + (sh ? 0 : x)) * ncl) * Cfg::CTAS + rank) * 128 + r;
         if (split && half == 0) {
           p.part_ml[prow * 2] = m_run;
-          p.part_ml[prow * 2 + 1] = l_row;
+          p.part_ml[prow * 2 + 1] = l_all;
         }
-        // output row of this thread, -1 for none
-        const int orow = hl < p.G && t < p.C ? (u.b * p.h_q + u.g * p.G + hl) * p.C + t : -1;
 #pragma unroll
         for (int c = 0; c < (u.j1 > u.j0 ? DH : 0); c += 32) {
           uint4 w4[4];                     // 32 output columns as bf16

@@ -181,9 +181,9 @@ quoka_status launch_window_simt(const Dims& d, const SeqTable& tab, long long ro
 }
 
 // Units per tile of the tensor-core form and the space of their partials.
-constexpr int WINDOW_STREAMS_PAIR = 148;      // two streams on each of 74 SM pairs
-constexpr int WINDOW_STREAMS_SINGLE = 296;    // two on each of 148 SMs
-constexpr int WINDOW_MIN_BLOCKS = 4;          // 128-key blocks per unit at least
+constexpr int WINDOW_PAIRS = 74;              // clusters of two SMs, whose two streams share a unit
+constexpr int WINDOW_SINGLES = 148;
+constexpr int WINDOW_MIN_BLOCKS = 8;          // 128-key blocks per unit at least
 constexpr int WINDOW_MAX_SPLIT = 32;
 
 struct WindowWs {
@@ -198,7 +198,7 @@ WindowWs window_tc_ws(const Dims& d, int max_prefix, int window) {
   const int ctas = pair ? 2 : 1, span = ctas * (128 / d.G);
   w.tiles = (long long)((d.C + span - 1) / span) * d.h_kv * d.batch;
   const long long blocks = (std::min<long long>(window, (long long)max_prefix + 1) + span + AWT_BK - 1) / AWT_BK;
-  const long long room = (pair ? WINDOW_STREAMS_PAIR : WINDOW_STREAMS_SINGLE) / w.tiles;
+  const long long room = (pair ? WINDOW_PAIRS : WINDOW_SINGLES) / w.tiles;
   w.nsplit = (int)std::max<long long>(1, std::min(std::min(room, blocks / WINDOW_MIN_BLOCKS), (long long)WINDOW_MAX_SPLIT));
   const size_t rows = w.nsplit > 1 ? (size_t)w.tiles * w.nsplit * ctas * 128 : 0;
   w.part = 0;
