@@ -65,19 +65,15 @@ __device__ __forceinline__ int stream_len(const StreamParams& p, const SeqTable&
   else return tab.prefix[b] + 1;
 }
 
-// base[b] = tiles of one KV head of the sequences before b; base[batch] the total.
-// Every thread of the block calls it.
-template <bool kPaged>
-__device__ void stream_bases(const StreamParams& p, const SeqTable& tab, int* base) {
-  for (int b = threadIdx.x; b < p.batch; b += blockDim.x)
-    base[b + 1] = key_span(stream_len<kPaged>(p, tab, b), p.window, p.n_sink).nt;
+// base[b] = tiles of one KV head of the sequences before b, from their lengths; base[batch]
+// the total.  Every thread of the block calls it; it ends with a block barrier.
+__device__ void stream_bases_of(const StreamParams& p, const int* lens, int* base) {
   if (threadIdx.x == 0) base[0] = 0;
-  __syncthreads();
   if (threadIdx.x < 32) {
     int run = 0;
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + threadIdx.x;
-      int x = b < p.batch ? base[b + 1] : 0;
+      int x = b < p.batch ? key_span(lens[b], p.window, p.n_sink).nt : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -89,6 +85,13 @@ __device__ void stream_bases(const StreamParams& p, const SeqTable& tab, int* ba
     }
   }
   __syncthreads();
+}
+// As above, reading the lengths first: lens and base are the block's shared memory.
+template <bool kPaged>
+__device__ void stream_bases(const StreamParams& p, const SeqTable& tab, int* lens, int* base) {
+  for (int b = threadIdx.x; b < p.batch; b += blockDim.x) lens[b] = stream_len<kPaged>(p, tab, b);
+  __syncthreads();
+  stream_bases_of(p, lens, base);
 }
 
 __device__ __forceinline__ int stream_start(int c, int ctas, int tiles) {
@@ -113,12 +116,11 @@ struct StreamSeg {
   bool whole;
   KeySpan span;
 };
-template <bool kPaged>
-__device__ __forceinline__ StreamSeg stream_seg(const StreamParams& p, const SeqTable& tab, const int* base, int x,
-                                                int x1) {
+__device__ __forceinline__ StreamSeg stream_seg_of(const StreamParams& p, const int* lens, const int* base, int x,
+                                                   int x1) {
   StreamSeg s;
   s.b = stream_seq(base, p.batch, p.h_kv, x);
-  s.span = key_span(stream_len<kPaged>(p, tab, s.b), p.window, p.n_sink);
+  s.span = key_span(lens[s.b], p.window, p.n_sink);
   const int r = x - base[s.b] * p.h_kv;
   s.g = r / s.span.nt;
   s.i0 = r - s.g * s.span.nt;
@@ -145,7 +147,7 @@ __device__ __forceinline__ void ast_cp16(void* dst, const void* src, bool on) {
 
 template <typename T, int D, int R>
 constexpr int ast_smem_bytes(int batch) {
-  return adc_smem_bytes<T, D, R>() + (batch + 1) * 4;
+  return adc_smem_bytes<T, D, R>() + (2 * batch + 1) * 4;
 }
 
 // CUDA-core form (fp32).  Warps take 32-key batches of the CTA's tiles in turn, each with
@@ -167,7 +169,8 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
   unsigned char* vstage = stage + 32 * ROW;
   float* ps = reinterpret_cast<float*>(stage + Cfg::STAGE);
   int* base = reinterpret_cast<int*>(smem + adc_smem_bytes<T, D, R>());
-  stream_bases<kPaged>(p, tab, base);
+  int* lens = base + p.batch + 1;
+  stream_bases<kPaged>(p, tab, lens, base);
 
   const int tiles = base[p.batch] * p.h_kv;
   const int ctas = min(p.ctas, tiles);                     // every share holds a tile at least
@@ -176,7 +179,7 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
   const int rows = min(R, p.G - r0);
   const int x0 = stream_start(c, ctas, tiles), x1 = stream_start(c + 1, ctas, tiles);
   for (int x = x0; x < x1;) {
-    const StreamSeg sg = stream_seg<kPaged>(p, tab, base, x, x1);
+    const StreamSeg sg = stream_seg_of(p, lens, base, x, x1);
     for (int e = threadIdx.x; e < R * D; e += blockDim.x) {
       const int r = e / D, d = e - r * D;
       qs[e] = r < rows ? to_f32(q[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + r0 + r) * D + d]) * p.scale_log2 : 0.f;
@@ -349,8 +352,8 @@ template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(ASJ_THREADS)
 attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab,
                         T* __restrict__ out) {
-  extern __shared__ int base[];                            // [batch + 1], then weights [N][G]
-  stream_bases<kPaged>(p, tab, base);
+  extern __shared__ int base[];                            // [batch + 1], lengths [batch], weights [N][G]
+  stream_bases<kPaged>(p, tab, base + p.batch + 1, base);
   const int tiles = base[p.batch] * p.h_kv, ctas = min(p.ctas, tiles);
   const int unit = blockIdx.x, b = unit / p.h_kv, g = unit - b * p.h_kv;
   const int nt = base[b + 1] - base[b];
@@ -358,7 +361,7 @@ attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_con
   const int c0 = stream_cta(s, ctas, tiles), c1 = stream_cta(s + nt - 1, ctas, tiles);
   if (c0 == c1) return;                                    // finished by its CTA
   const int nc = c1 - c0 + 1;
-  float* fw = reinterpret_cast<float*>(base + p.batch + 1);
+  float* fw = reinterpret_cast<float*>(base + 2 * p.batch + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int r = warp; r < p.G; r += ASJ_THREADS / 32) {
     float M = -INFINITY, L = 0.f;
@@ -403,11 +406,12 @@ attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_con
 // The add is a reduction in memory, so a page that two sequences share gets both sums.
 __global__ void __launch_bounds__(AST_TILE)
 attn_stream_record_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab) {
-  extern __shared__ int base[];
-  stream_bases<true>(p, tab, base);
+  extern __shared__ int base[];                            // [batch + 1], lengths [batch]
+  const int* lens = base + p.batch + 1;
+  stream_bases<true>(p, tab, base + p.batch + 1, base);
   const int tiles = base[p.batch] * p.h_kv;
   for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
-    const StreamSeg sg = stream_seg<true>(p, tab, base, x, x + 1);
+    const StreamSeg sg = stream_seg_of(p, lens, base, x, x + 1);
     const int j = sg.span.tile(sg.i0) * AST_TILE + threadIdx.x;
     if (!sg.span.visible(j)) continue;
     const float* lg = p.logits + ((size_t)x * AST_TILE + threadIdx.x) * p.G;

@@ -103,6 +103,49 @@ cudaError_t launch_stream_simt(const StreamParams& p, const SeqTable& tab, const
   return cudaGetLastError();
 }
 
+// fp32: query heads of a group in rows of up to 16 per CTA, as many CTAs as fit the SMs at once.
+template <typename T, int D, bool kPaged>
+cudaError_t launch_stream_rows(StreamParams& p, const SeqTable& tab, int max_ctas, const void* q, const void* k,
+                               const void* v, void* out, cudaStream_t st) {
+  int r = 1;
+  while (r < std::min(p.G, 16)) r *= 2;
+  const int per_sm = std::max(1, std::min(4, 230000 / (ast_smem_bytes<T, D, 16>(p.batch) + 1024)));
+  p.ctas = std::min(max_ctas, sm_count() * per_sm);
+  switch (r) {
+    case 1: return launch_stream_simt<T, D, 1, kPaged>(p, tab, q, k, v, out, st);
+    case 2: return launch_stream_simt<T, D, 2, kPaged>(p, tab, q, k, v, out, st);
+    case 4: return launch_stream_simt<T, D, 4, kPaged>(p, tab, q, k, v, out, st);
+    case 8: return launch_stream_simt<T, D, 8, kPaged>(p, tab, q, k, v, out, st);
+    default: return launch_stream_simt<T, D, 16, kPaged>(p, tab, q, k, v, out, st);
+  }
+}
+
+// bf16: one CTA per SM.
+template <int D, int N, bool kPaged>
+quoka_status launch_stream_tc(StreamParams& p, const SeqTable& tab, int max_ctas, const void* q, const void* k,
+                              const void* v, void* out, cudaStream_t st) {
+  p.ctas = std::min(max_ctas, sm_count());
+  int box = AST_TILE;                    // rows per copy: a power of two that divides the pages
+  uint64_t rows = (uint64_t)p.h_kv * p.kv.rows_per_head;
+  if (kPaged) {
+    while (p.kv.page_size % box) box /= 2;
+    rows = (uint64_t)p.kv.num_pages * p.h_kv * p.kv.page_size;
+  }
+  CUtensorMap qmap, kmap, vmap;
+  quoka_status s;
+  if ((s = make_map_bf16(&qmap, q, (uint64_t)p.batch * p.h_q, D, 64, N, "q")) != QUOKA_OK) return s;
+  if ((s = make_map_bf16(&kmap, k, rows, D, 64, box, "keys")) != QUOKA_OK) return s;
+  if ((s = make_map_bf16(&vmap, v, rows, D, 64, box, "values")) != QUOKA_OK) return s;
+  const int smem = Stc2Cfg<D, N>::smem(p.batch);
+  cudaError_t e = ensure_smem(attn_stream_tc_kernel<D, N, kPaged>, smem);
+  if (e != cudaSuccess) return cuda_fail(e, "attn_stream_tc smem");
+  attn_stream_tc_kernel<D, N, kPaged><<<p.ctas, STC2_THREADS, smem, st>>>(qmap, kmap, vmap, p, tab, box,
+                                                                          reinterpret_cast<__nv_bfloat16*>(out));
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attn_stream_tc launch");
+  prof_mark(st, "attn_stream_tc_kernel");
+  return QUOKA_OK;
+}
+
 template <typename T, int D, bool kPaged>
 quoka_status launch_stream(const Dims& d, const SeqTable& tab, StreamParams p, const StreamWs& w, const void* q,
                            const void* k, const void* v, void* out, unsigned char* ws, cudaStream_t st) {
@@ -116,28 +159,24 @@ quoka_status launch_stream(const Dims& d, const SeqTable& tab, StreamParams p, c
   p.unit_ml = reinterpret_cast<float*>(ws + w.unit_ml);
   p.logits = p.record ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
   cudaError_t e;
-  int r = 1;
-  while (r < std::min(d.G, 16)) r *= 2;
-  // as many CTAs as fit the SMs at once
-  const int per_sm = std::max(1, std::min(4, 230000 / (ast_smem_bytes<T, D, 16>(d.batch) + 1024)));
-  p.ctas = std::min(w.ctas, sm_count() * per_sm);
-  switch (r) {
-    case 1: e = launch_stream_simt<T, D, 1, kPaged>(p, tab, q, k, v, out, st); break;
-    case 2: e = launch_stream_simt<T, D, 2, kPaged>(p, tab, q, k, v, out, st); break;
-    case 4: e = launch_stream_simt<T, D, 4, kPaged>(p, tab, q, k, v, out, st); break;
-    case 8: e = launch_stream_simt<T, D, 8, kPaged>(p, tab, q, k, v, out, st); break;
-    default: e = launch_stream_simt<T, D, 16, kPaged>(p, tab, q, k, v, out, st); break;
+  if constexpr (sizeof(T) == 2) {
+    const quoka_status s = d.G <= 16   ? launch_stream_tc<D, 16, kPaged>(p, tab, w.ctas, q, k, v, out, st)
+                           : d.G <= 32 ? launch_stream_tc<D, 32, kPaged>(p, tab, w.ctas, q, k, v, out, st)
+                                       : launch_stream_tc<D, 64, kPaged>(p, tab, w.ctas, q, k, v, out, st);
+    if (s != QUOKA_OK) return s;
+  } else {
+    if ((e = launch_stream_rows<T, D, kPaged>(p, tab, w.ctas, q, k, v, out, st)) != cudaSuccess)
+      return cuda_fail(e, "attn_stream launch");
+    prof_mark(st, "attn_stream_kernel");
   }
-  if (e != cudaSuccess) return cuda_fail(e, "attn_stream launch");
-  prof_mark(st, "attn_stream_kernel");
-  const int jsmem = (d.batch + 1 + std::min(p.ctas, w.max_unit_tiles) * d.G) * 4;
+  const int jsmem = (2 * d.batch + 1 + std::min(p.ctas, w.max_unit_tiles) * d.G) * 4;
   if ((e = ensure_smem(attn_stream_join_kernel<T, D, kPaged>, jsmem)) != cudaSuccess) return cuda_fail(e, "join smem");
   attn_stream_join_kernel<T, D, kPaged><<<d.batch * d.h_kv, ASJ_THREADS, jsmem, st>>>(p, tab, reinterpret_cast<T*>(out));
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attn_stream_join launch");
   prof_mark(st, "attn_stream_join_kernel");
   if (p.record) {
     const int grid = (int)std::min<long long>(w.max_tiles, (long long)sm_count() * 16);
-    attn_stream_record_kernel<<<grid, AST_TILE, (d.batch + 1) * 4, st>>>(p, tab);
+    attn_stream_record_kernel<<<grid, AST_TILE, (2 * d.batch + 1) * 4, st>>>(p, tab);
     if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attn_stream_record launch");
     prof_mark(st, "attn_stream_record_kernel");
   }

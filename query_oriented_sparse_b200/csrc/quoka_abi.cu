@@ -30,6 +30,7 @@
 #include "attn_window.cuh"
 #include "attn_window_tc.cuh"
 #include "attn_stream.cuh"
+#include "attn_stream_tc.cuh"
 
 using namespace quoka;
 
