@@ -339,7 +339,7 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
   }
 }
 
-constexpr int ASJ_THREADS = 256;
+constexpr int ASJ_ROWS = 8;                // output rows (warps) per block of the join
 
 // Slot of CTA c's partial of a unit whose tiles start at s: the CTA's first segment when
 // its share starts inside the unit, else its last.
@@ -347,59 +347,70 @@ __device__ __forceinline__ int stream_slot(int c, int s, int ctas, int tiles) {
   return 2 * c + (stream_start(c, ctas, tiles) >= s ? 0 : 1);
 }
 
-// One block per (sequence, KV head): out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M).
+// One warp per output row (sequence, query head): out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M)
+// over the CTAs that share its (sequence, KV head).
 template <typename T, int D, bool kPaged>
-__global__ void __launch_bounds__(ASJ_THREADS)
+__global__ void __launch_bounds__(ASJ_ROWS * 32)
 attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab,
                         T* __restrict__ out) {
-  extern __shared__ int base[];                            // [batch + 1], lengths [batch], weights [N][G]
+  extern __shared__ int base[];                            // [batch + 1], lengths [batch]
   stream_bases<kPaged>(p, tab, base + p.batch + 1, base);
   const int tiles = base[p.batch] * p.h_kv, ctas = min(p.ctas, tiles);
-  const int unit = blockIdx.x, b = unit / p.h_kv, g = unit - b * p.h_kv;
+  const int row = blockIdx.x * ASJ_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= p.batch * p.h_q) return;
+  const int unit = row / p.G, r = row - unit * p.G;
+  const int b = unit / p.h_kv, g = unit - b * p.h_kv;
   const int nt = base[b + 1] - base[b];
   const int s = base[b] * p.h_kv + g * nt;
-  const int c0 = stream_cta(s, ctas, tiles), c1 = stream_cta(s + nt - 1, ctas, tiles);
-  if (c0 == c1) return;                                    // finished by its CTA
-  const int nc = c1 - c0 + 1;
-  float* fw = reinterpret_cast<float*>(base + 2 * p.batch + 1);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int r = warp; r < p.G; r += ASJ_THREADS / 32) {
-    float M = -INFINITY, L = 0.f;
-    for (int i = lane; i < nc; i += 32) {
-      const float* ml = p.part_ml + ((size_t)stream_slot(c0 + i, s, ctas, tiles) * p.G + r) * 2;
-      if (ml[1] != 0.f) M = fmaxf(M, ml[0]);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    for (int i = lane; i < nc; i += 32) {
-      const float* ml = p.part_ml + ((size_t)stream_slot(c0 + i, s, ctas, tiles) * p.G + r) * 2;
-      const float f = ml[1] != 0.f ? exp2f(ml[0] - M) : 0.f;   // a partial without visible keys weighs 0
-      fw[i * p.G + r] = f;
-      L += ml[1] * f;
-    }
-    L = warp_sum(L);
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    for (int i = lane; i < nc; i += 32) fw[i * p.G + r] *= inv;
-    if (lane == 0 && p.logits) {
-      p.unit_ml[((size_t)unit * p.G + r) * 2] = M;
-      p.unit_ml[((size_t)unit * p.G + r) * 2 + 1] = inv;
-    }
+  const int c0 = stream_cta(s, ctas, tiles), nc = stream_cta(s + nt - 1, ctas, tiles) - c0 + 1;
+  if (nc == 1) return;                                     // finished by its CTA
+  auto part_row = [&](int i) { return (size_t)stream_slot(c0 + i, s, ctas, tiles) * p.G + r; };
+  float M = -INFINITY, L = 0.f;
+  for (int i = lane; i < nc; i += 32) {
+    const float* ml = p.part_ml + part_row(i) * 2;
+    if (ml[1] != 0.f) M = fmaxf(M, ml[0]);
   }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.G * D; e += ASJ_THREADS) {
-    const int r = e / D, d = e - r * D;
-    float o = 0.f;
-    for (int i0 = 0; i0 < nc; i0 += 8) {
-      float xs[8];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  constexpr int E = D / 32;                                // output elements per lane
+  float o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int i0 = 0; i0 < nc; i0 += 32) {
+    // lane i: partial i0 + i and its weight (0 for one without visible keys, whose O is not read)
+    const size_t mine = i0 + lane < nc ? part_row(i0 + lane) : 0;
+    float f = 0.f;
+    if (i0 + lane < nc) {
+      const float ml = p.part_ml[mine * 2], ll = p.part_ml[mine * 2 + 1];
+      f = ll != 0.f ? exp2f(ml - M) : 0.f;
+      if (ll != 0.f) L = fmaf(ll, f, L);
+    }
+    const int lim = min(32, nc - i0);
+    for (int i = 0; i < lim; i += 8) {
+      float xs[8][E], fs[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const size_t pr = __shfl_sync(0xffffffffu, (unsigned long long)mine, (i + u) & 31);
+        fs[u] = __shfl_sync(0xffffffffu, f, (i + u) & 31);
+        if (i + u >= lim) fs[u] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) xs[u][e] = 0.f;
+        if (fs[u] != 0.f) load_vec<float, E>(p.part + pr * D + lane * E, xs[u]);
+      }
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        xs[u] = i0 + u < nc ? p.part[((size_t)stream_slot(c0 + i0 + u, s, ctas, tiles) * p.G + r) * D + d] : 0.f;
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
-        if (i0 + u < nc && fw[(i0 + u) * p.G + r] != 0.f) o = fmaf(xs[u], fw[(i0 + u) * p.G + r], o);
+        for (int e = 0; e < E; ++e) o[e] = fs[u] != 0.f ? fmaf(xs[u][e], fs[u], o[e]) : o[e];
     }
-    out[((size_t)b * p.h_q + (size_t)g * p.G + r) * D + d] = from_f32<T>(o);
   }
+  L = warp_sum(L);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  if (lane == 0 && p.logits) {
+    p.unit_ml[(size_t)row * 2] = M;
+    p.unit_ml[(size_t)row * 2 + 1] = inv;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) out[(size_t)row * D + lane * E + e] = from_f32<T>(o[e] * inv);
 }
 
 // record[key] += sum over the group's heads of 2^(s - M) / L.  One thread per key of a tile.

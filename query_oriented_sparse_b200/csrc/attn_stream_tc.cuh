@@ -6,26 +6,32 @@
 //   S [128 keys x N]  = K_tile Q^T          (A = K tile, K-major; B = Q)
 //   O^T [128 dims x N] += V_tile^T P^T      (A = V tile, MN-major; B = P^T from shared memory)
 // (d = 64: rows 64-127 of O^T are computed over the K tile behind V and never read).  The
-// kernel is bound by HBM: a tile is 64 KB (d = 128) and an SM's share of the bandwidth brings
-// one in about 1.5 us, twice what the chain S -> softmax -> P.V takes.  So one tile is worked
-// on at a time while TMA fills the ring's other stages; what counts is that the loads never
-// pause, which the even split of the tiles and the stages ahead see to.
+// kernel is bound by HBM: a tile is 64 KB (d = 128), and an SM's share of the bandwidth brings
+// one in about 1.5 us.  What counts is that the loads never pause, which the even split of the
+// tiles and the ring's stages see to, and that the chain S -> softmax -> P.V keeps up, which
+// takes two softmax groups: for N = 16 they take the tiles in turn, each with its own maximum,
+// sum and O^T, joined at the end of a segment; for more rows, where a tile's exponentials
+// weigh more than its barriers, each takes half of the rows of every tile.
 //
 // Warp 0 loads: pages are copied box by box (a box is the largest power of two of rows that
 // divides the page size, at most 128), only boxes with a visible key, and marks the boxes
-// whose page was bad.  Warp 1 issues S, warp 6 P.V, warps 2-5 run the softmax, one thread per
-// key: its N logits come with one TMEM load.  The running maximum is common to the tile's keys
-// and only moves when some logit exceeds it by 2^8 (one barrier with an or-reduction tells);
-// then O^T is rescaled in TMEM.  Row sums are kept per thread and added up at the end of a
-// segment.  V rows of keys that are not visible are zeroed in shared memory, since 0 * NaN
-// would reach the sum; masked logits are replaced by selection.
+// whose page was bad.  A paged box is one copy: the tensor map splits rows into groups of
+// eight and their two 128-byte halves, so that the copy lays down whole swizzle atoms
+// [group][half][8 rows] (two copies per 16-row page and operand, instead of four, took the
+// 32-sequence decode step with pages of 16 from PAGEFIG).  Warp 1 issues S, warp 10 P.V, warps
+// 2-9 run the softmax, one thread per key: its logits come with one TMEM load.  The running
+// maximum is common to the tile's keys and only moves when some logit exceeds it by 2^8 (one
+// barrier with an or-reduction tells); then O^T is rescaled in TMEM.  Row sums are kept per
+// thread and added up at the end of a segment.  V rows of keys that are not visible are zeroed
+// in shared memory, since 0 * NaN would reach the sum; masked logits are replaced by
+// selection.  P is rounded to bf16 for its MMA (the sums are taken before).
 #pragma once
 #include "tc_ptx.cuh"
 #include "attn_stream.cuh"
 
 namespace quoka {
 
-constexpr int STC2_THREADS = 224;         // warp 0 load, 1 S, 2-5 softmax, 6 P.V
+constexpr int STC2_THREADS = 352;         // warp 0 load, 1 S, 2-9 softmax, 10 P.V
 constexpr float STC2_RESCALE_LOG2 = 8.0f;
 
 template <int D, int N>
@@ -37,10 +43,13 @@ struct Stc2Cfg {
   static constexpr int QB = N == 16 ? 2 : 1;        // Q buffers
   static constexpr int Q_BYTES = N * D * 2;
   static constexpr int P_BYTES = N * AST_TILE * 2;
-  static constexpr int TMEM = N == 16 ? 64 : N == 32 ? 128 : 256;   // S twice, O^T
+  static constexpr bool BYROW = N > 16;             // the softmax groups share rows, not tiles
+  static constexpr int NR = BYROW ? N / 2 : N;      // rows per thread
+  static constexpr int TMEM = N == 64 ? 256 : N == 32 ? 128 : 64;   // S twice, then O^T (one per group)
+  static constexpr int OB = BYROW ? 0 : (N * 128 + 2 * N) * 4;      // group 1's O^T, m and l of a segment
   // kfull, vfull, empty per stage; qfull[2], qempty[2], sfull[2], pready[2], pfree[2]
   static constexpr int NBAR = 3 * NST + 10;
-  static constexpr int FIXED = NST * STAGE + QB * Q_BYTES + 2 * P_BYTES + NBAR * 8 + 16 + NST * 4 + 4 * N * 4 * 2 + 64;
+  static constexpr int FIXED = NST * STAGE + QB * Q_BYTES + 2 * P_BYTES + NBAR * 8 + 16 + NST * 4 + 16 * NR * 4 + OB + 64;
   static constexpr int smem(int batch) { return 1024 + FIXED + (2 * batch + 1) * 4; }
 };
 
@@ -65,6 +74,8 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
                       const __grid_constant__ SeqTable tab, int box /* rows per TMA box */, __nv_bfloat16* __restrict__ out) {
   using Cfg = Stc2Cfg<D, N>;
   constexpr int KB = Cfg::KB, NST = Cfg::NST, QB = Cfg::QB;
+  // bytes between a tile's groups of eight rows, and between their 128-byte halves
+  constexpr int GS = kPaged ? 1024 * KB : 1024, HS = kPaged ? 1024 : 16384;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_u32 = ptx::smem_u32(smem_raw);
   uint8_t* smem = smem_raw + (((raw_u32 + 1023u) & ~1023u) - raw_u32);
@@ -81,8 +92,9 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   uint64_t* pfree = pready + 2;                     // P.V has read P
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(pfree + 2);
   uint32_t* boxes = tmem_slot + 4;                  // [stage] bit i: box i of the tile was loaded
-  float* wred = reinterpret_cast<float*>(boxes + ((NST + 3) & ~3));   // [4 warps][N]
-  int* base = reinterpret_cast<int*>(wred + 2 * 4 * N);
+  float* wred = reinterpret_cast<float*>(boxes + ((NST + 3) & ~3));   // [maxima, sums][8 warps][rows]
+  float* obuf = wred + 16 * Cfg::NR;                   // [row][dimension], then m, l
+  int* base = reinterpret_cast<int*>(obuf + Cfg::OB / 4);
   int* lens = base + p.batch + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -95,7 +107,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       ptx::mbar_init(&qfull[s], 1);
       ptx::mbar_init(&qempty[s], 1);
       ptx::mbar_init(&sfull[s], 1);
-      ptx::mbar_init(&pready[s], 4);
+      ptx::mbar_init(&pready[s], Cfg::BYROW ? 8 : 4);
       ptx::mbar_init(&pfree[s], 1);
     }
     ptx::fence_mbar_init();
@@ -159,14 +171,23 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
         __syncwarp();
         uint8_t* sV = sKV + st * Cfg::STAGE;
-        // K boxes first, then V: copy e is box e % nb, 128-byte block (e / nb) % KB, of K or V
-        for (int e = lane; e < ((2 * KB * nb + 31) & ~31); e += 32) {
-          const int bi = e % nb, kb = (e / nb) % KB;
-          const bool isv = e >= KB * nb;
+        if constexpr (kPaged) {
+          // lane e < nb: K of box e; lane e + 16: its V
+          const int bi = lane & 15;
           const int r = __shfl_sync(0xffffffffu, row, bi);
-          if (e < 2 * KB * nb && ((set >> bi) & 1u))
-            ptx::tma_load_2d(sV + (isv ? 0 : Cfg::T_BYTES) + kb * 16384 + bi * box * 128, isv ? &vmap : &kmap,
-                             isv ? &vfull[st] : &kfull[st], kb * 64, r);
+          if (bi < nb && ((set >> bi) & 1u)) {
+            const bool isv = lane >= 16;
+            ptx::tma_load_4d(sV + (isv ? 0 : Cfg::T_BYTES) + bi * box * D * 2, isv ? &vmap : &kmap,
+                             isv ? &vfull[st] : &kfull[st], 0, 0, 0, r >> 3);
+          }
+        } else {
+          // one box: lane e < KB: half e of K; lane e + KB: of V
+          const int r = __shfl_sync(0xffffffffu, row, 0);
+          if (lane < 2 * KB && set) {
+            const bool isv = lane >= KB;
+            ptx::tma_load_2d(sV + (isv ? 0 : Cfg::T_BYTES) + (lane % KB) * 16384, isv ? &vmap : &kmap,
+                             isv ? &vfull[st] : &kfull[st], (lane % KB) * 64, r);
+          }
         }
       }
       x += sg.cnt;
@@ -188,11 +209,11 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           ptx::tc_fence_after();
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
-            const uint32_t a0 = ptx::smem_u32(sKV + st * Cfg::STAGE + Cfg::T_BYTES + kb * 16384);
+            const uint32_t a0 = ptx::smem_u32(sKV + st * Cfg::STAGE + Cfg::T_BYTES + kb * HS);
             const uint32_t b0 = ptx::smem_u32(sQ + (sn % QB) * Cfg::Q_BYTES + kb * N * 128);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
-              ptx::mma_bf16_ss(tmem + (uint32_t)(buf * N), ptx::sdesc_sw128(a0 + ks * 32, 16, 1024),
+              ptx::mma_bf16_ss(tmem + (uint32_t)(buf * N), ptx::sdesc_sw128(a0 + ks * 32, 16, GS),
                                ptx::sdesc_sw128(b0 + ks * 32, 16, 1024), idesc, (kb | ks) ? 1u : 0u);
           }
           ptx::tc_commit(&sfull[buf]);
@@ -201,7 +222,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         x += sg.cnt;
       }
     }
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     // ---------------- O^T += V^T P^T ----------------
     if (lane == 0) {
       const uint32_t idesc = ptx::idesc_bf16(128, N, false) | (1u << 15);   // A is MN-major
@@ -219,9 +240,10 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           const uint32_t b0 = ptx::smem_u32(sP + buf * Cfg::P_BYTES);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)                    // 16 keys per MMA
-            ptx::mma_bf16_ss(tmem + 2 * N, ptx::sdesc_sw128(a0 + ks * 2048, 16384, 1024),
+            ptx::mma_bf16_ss(tmem + (uint32_t)(2 * N + (Cfg::BYROW ? 0 : buf * N)),
+                             ptx::sdesc_sw128(a0 + ks * 2 * GS, KB == 1 ? 16384 : HS, GS),
                              ptx::sdesc_sw128(b0 + (ks >> 2) * (N * 128) + (ks & 3) * 32, 16, 1024), idesc,
-                             (i | ks) ? 1u : 0u);
+                             (i >= (Cfg::BYROW ? 1 : 2) || ks > 0) ? 1u : 0u);
           ptx::tc_commit(&empty[st]);
           ptx::tc_commit(&pfree[buf]);
         }
@@ -230,89 +252,103 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     }
   } else {
     // ---------------- softmax: thread = key of the tile, and dimension of O^T ----------------
+    constexpr bool BYROW = Cfg::BYROW;
+    constexpr int NR = Cfg::NR;
+    const int grp = (warp - 2) >> 2;
+    const int r_lo = BYROW ? grp * NR : 0;                  // this group's rows
+    const int rows = min(NR, p.G - r_lo);                   // (may be <= 0)
     const int quarter = warp & 3;
     const int kk = quarter * 32 + lane;
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t o_addr = tmem + lane_off + 2 * N;
+    const uint32_t o_addr = tmem + lane_off + (uint32_t)(2 * N + grp * NR);
     // this key's place in P^T: 64-key block, then row r of 128 bytes, 16-byte chunks swizzled
-    uint8_t* p_key = sP + (kk >> 6) * (N * 128) + (kk & 7) * 2;
+    uint8_t* p_key = sP + (kk >> 6) * (N * 128) + (kk & 7) * 2 + r_lo * 128;   // (r_lo is a multiple of 8)
     const int p_chunk = (kk & 63) >> 3;
+    float* wmax = wred + grp * 4 * NR;
+    float* wsum = wred + 8 * NR + grp * 4 * NR;
+    const int bar_g = 1 + grp;                              // this group's barrier
     bool ok = true;
     int n = 0;
     // Every warp of the group reaches every barrier of every tile and segment: after a failed
     // (timed-out) wait it skips the work but not the barriers.
     for (int x = x0; x < x1;) {
       const StreamSeg sg = seg_at(x);
-      float m[N], l[N];
+      float m[NR], l[NR];
 #pragma unroll
-      for (int r = 0; r < N; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
+      for (int r = 0; r < NR; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
+      bool started = false;                                 // O^T holds earlier tiles of the segment
       for (int i = 0; i < sg.cnt; ++i, ++n) {
         const int st = n % NST, buf = n & 1;
+        if (!BYROW && buf != grp) continue;
+        const uint32_t ph = (uint32_t)(n >> 1) & 1u;
         const int j = sg.span.tile(sg.i0 + i) * AST_TILE + kk;
         bool vis = false;
-        float s[N];
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&sfull[buf], (uint32_t)(n >> 1) & 1u) &&
+        float s[NR];
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&sfull[buf], ph) &&
                                                  ptx::mbar_wait_sleep(&kfull[st], (uint32_t)(n / NST) & 1u));
         if (ok) {
           ptx::tc_fence_after();
 #pragma unroll
-          for (int r0 = 0; r0 < N; r0 += 16) {
+          for (int r0 = 0; r0 < NR; r0 += 16) {
             uint32_t w[16];
-            ptx::tmem_ld16(tmem + lane_off + (uint32_t)(buf * N + r0), w);
+            ptx::tmem_ld16(tmem + lane_off + (uint32_t)(buf * N + r_lo + r0), w);
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r0 + r] = __uint_as_float(w[r]);
           }
-          ptx::tmem_ld_wait();
           vis = sg.span.visible(j) && ((boxes[st] >> (kk / box)) & 1u);
+          ptx::tmem_ld_wait();
         }
         bool up = false;
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
+        for (int r = 0; r < NR; ++r) {
           s[r] = vis ? s[r] * p.scale_log2 : -INFINITY;
-          if (r < p.G) up = up || s[r] > m[r] + STC2_RESCALE_LOG2;   // (m = -inf: any visible key)
+          if (r < rows) up = up || s[r] > m[r] + STC2_RESCALE_LOG2;   // (m = -inf: any visible key)
         }
         if (p.logits) {
-          float* lg = p.logits + ((size_t)(x + i) * AST_TILE + kk) * p.G;
+          float* lg = p.logits + ((size_t)(x + i) * AST_TILE + kk) * p.G + r_lo;
           if ((p.G & 3) == 0) {
 #pragma unroll
-            for (int r = 0; r < N; r += 4)
-              if (r < p.G) *reinterpret_cast<float4*>(lg + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
+            for (int r = 0; r < NR; r += 4)
+              if (r < rows) *reinterpret_cast<float4*>(lg + r) = make_float4(s[r], s[r + 1], s[r + 2], s[r + 3]);
           } else {
 #pragma unroll
-            for (int r = 0; r < N; ++r)
-              if (r < p.G) lg[r] = s[r];
+            for (int r = 0; r < NR; ++r)
+              if (r < rows) lg[r] = s[r];
           }
         }
-        if (named_bar_or(1, 128, up)) {
+        // P.V two tiles back (of this P buffer) is done; by tiles, it was this group's last one
+        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&pfree[buf], ph ^ 1u));
+        if (named_bar_or(bar_g, 128, up)) {
           // the tile's maxima, and O^T and the sums rescaled to them
 #pragma unroll
-          for (int r = 0; r < N; ++r) {
-            if (r >= p.G) break;
+          for (int r = 0; r < NR; ++r) {
+            if (r >= rows) break;
             float v = s[r];
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == (r & 31)) wred[quarter * N + r] = v;
+            if (lane == (r & 31)) wmax[quarter * NR + r] = v;
           }
-          ptx::named_bar(2, 128);
-          float al[N];
+          ptx::named_bar(bar_g, 128);
+          float al[NR];
 #pragma unroll
-          for (int r = 0; r < N; ++r) {
+          for (int r = 0; r < NR; ++r) {
             al[r] = 1.f;
-            if (r >= p.G) continue;
-            const float mn = fmaxf(fmaxf(fmaxf(wred[r], wred[N + r]), fmaxf(wred[2 * N + r], wred[3 * N + r])), m[r]);
+            if (r >= rows) continue;
+            const float mn = fmaxf(fmaxf(fmaxf(wmax[r], wmax[NR + r]), fmaxf(wmax[2 * NR + r], wmax[3 * NR + r])), m[r]);
             if (mn > m[r]) {
               al[r] = ptx::ex2_approx(m[r] - mn);           // m = -inf: 0
               m[r] = mn;
               l[r] *= al[r];
             }
           }
-          if (i > 0 && ok) {
-            // O^T holds the segment's earlier tiles once P.V of the last one is done
-            ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&empty[(n - 1) % NST], (uint32_t)((n - 1) / NST) & 1u));
-            if (ok) ptx::tc_fence_after();
+          if (started && ok) {
+            if constexpr (BYROW) {                          // P.V of the tile before
+              ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&pfree[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u));
+            }
+            ptx::tc_fence_after();
 #pragma unroll
-            for (int r0 = 0; r0 < N; r0 += 16) {
-              if (r0 >= p.G || !ok) break;
+            for (int r0 = 0; r0 < NR; r0 += 16) {
+              if (r0 >= rows || !ok) break;
               uint32_t w[16];
               ptx::tmem_ld16(o_addr + (uint32_t)r0, w);
               ptx::tmem_ld_wait();
@@ -322,24 +358,24 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             }
             ptx::tmem_st_wait();
           }
-          ptx::named_bar(2, 128);                           // wred is free again
+          ptx::named_bar(bar_g, 128);                       // wmax is free again
         }
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&pfree[buf], ((uint32_t)(n >> 1) & 1u) ^ 1u));
         if (!ok) continue;
+        started = true;
 #pragma unroll
-        for (int r = 0; r < N; ++r) {
-          if (r >= p.G) break;
+        for (int r = 0; r < NR; ++r) {
+          if (r >= rows) break;
           // (a row whose keys so far are all masked has m = -inf and weights 0)
           const float pr = m[r] == -INFINITY ? 0.f : ptx::ex2_approx(s[r] - m[r]);
           l[r] += pr;
           *reinterpret_cast<__nv_bfloat16*>(p_key + buf * Cfg::P_BYTES + r * 128 + ((p_chunk ^ (r & 7)) << 4)) =
               __float2bfloat16_rn(pr);
         }
-        if (!vis) {                                         // P.V must not meet what lies there
+        if (!vis && (!BYROW || grp == 0)) {                 // P.V must not meet what lies there
           (void)ptx::mbar_wait_sleep(&vfull[st], (uint32_t)(n / NST) & 1u);
 #pragma unroll
           for (int kb = 0; kb < KB; ++kb) {
-            uint4* v4 = reinterpret_cast<uint4*>(sKV + st * Cfg::STAGE + kb * 16384 + kk * 128);
+            uint4* v4 = reinterpret_cast<uint4*>(sKV + st * Cfg::STAGE + (kk >> 3) * GS + kb * HS + (kk & 7) * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v4[e] = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -350,50 +386,84 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         if (lane == 0) ptx::mbar_arrive(&pready[buf]);
       }
 
-      // the segment's sums and O^T: out when the unit is whole, else a partial
+      // the segment's sums, and its last P.V of this group
 #pragma unroll
-      for (int r = 0; r < N; ++r) {
-        if (r >= p.G) break;
+      for (int r = 0; r < NR; ++r) {
+        if (r >= rows) break;
         const float v = warp_sum(l[r]);
-        if (lane == (r & 31)) wred[(4 + quarter) * N + r] = v;
+        if (lane == (r & 31)) wsum[quarter * NR + r] = v;
       }
-      if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&empty[(n - 1) % NST], (uint32_t)((n - 1) / NST) & 1u));
-      ptx::named_bar(2, 128);
-      if (ok) {
-        ptx::tc_fence_after();
-        const float* lw = wred + 4 * N;
-        const int slot = 2 * c + (x == x0 ? 0 : 1);
+      if (ok && started) {
+        const int nl = BYROW || ((n - 1) & 1) == grp ? n - 1 : n - 2;
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&pfree[nl & 1], (uint32_t)(nl >> 1) & 1u));
+      }
+      ptx::named_bar(bar_g, 128);
+      ptx::tc_fence_after();
+      const int slot = 2 * c + (x == x0 ? 0 : 1);
+      auto finish = [&](int r, float o, float M, float L) {  // row r_lo + r, dimension kk
+        const int row = r_lo + r;
+        if (sg.whole) {
+          if (kk < D)
+            out[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + row) * D + kk] = __float2bfloat16_rn(L == 0.f ? 0.f : o / L);
+          if (kk == 0 && p.logits) {
+            p.unit_ml[((size_t)sg.unit * p.G + row) * 2] = M;
+            p.unit_ml[((size_t)sg.unit * p.G + row) * 2 + 1] = L == 0.f ? 0.f : 1.f / L;
+          }
+        } else {
+          if (kk < D) p.part[((size_t)slot * p.G + row) * D + kk] = o;
+          if (kk == 0) {
+            p.part_ml[((size_t)slot * p.G + row) * 2] = M;
+            p.part_ml[((size_t)slot * p.G + row) * 2 + 1] = L;
+          }
+        }
+      };
 #pragma unroll
-        for (int r0 = 0; r0 < N; r0 += 16) {
-          if (r0 >= p.G) break;
-          uint32_t w[16];
-          ptx::tmem_ld16(o_addr + (uint32_t)r0, w);
-          ptx::tmem_ld_wait();
+      for (int r0 = 0; r0 < NR; r0 += 16) {
+        if (r0 >= rows) break;
+        uint32_t w[16];
+        ptx::tmem_ld16(o_addr + (uint32_t)r0, w);
+        ptx::tmem_ld_wait();
+        if constexpr (BYROW) {
 #pragma unroll
           for (int ri = 0; ri < 16; ++ri) {
             const int r = r0 + ri;
-            if (r >= p.G) break;
-            const float L = (lw[r] + lw[N + r]) + (lw[2 * N + r] + lw[3 * N + r]);
-            const float o = __uint_as_float(w[ri]);
-            if (sg.whole) {
-              if (kk < D)
-                out[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + r) * D + kk] = __float2bfloat16_rn(L == 0.f ? 0.f : o / L);
-              if (kk == 0 && p.logits) {
-                p.unit_ml[((size_t)sg.unit * p.G + r) * 2] = m[r];
-                p.unit_ml[((size_t)sg.unit * p.G + r) * 2 + 1] = L == 0.f ? 0.f : 1.f / L;
-              }
-            } else {
-              if (kk < D) p.part[((size_t)slot * p.G + r) * D + kk] = o;
+            if (r >= rows || !ok) break;
+            const float L = (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]);
+            finish(r, __uint_as_float(w[ri]), m[r], L);
+          }
+        } else {
+          // group 1 leaves its half of the segment's tiles, group 0 joins it to its own
+          float* ml = obuf + N * 128;
+          if (grp == 1) {
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+              if (r >= rows) break;
+              obuf[r * 128 + kk] = __uint_as_float(w[r]);
               if (kk == 0) {
-                p.part_ml[((size_t)slot * p.G + r) * 2] = m[r];
-                p.part_ml[((size_t)slot * p.G + r) * 2 + 1] = L;
+                ml[r] = m[r];
+                ml[N + r] = ok ? (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]) : 0.f;
               }
             }
           }
+          ptx::named_bar(3, 256);
+          if (grp == 0) {
+#pragma unroll
+            for (int r = 0; r < N; ++r) {
+              if (r >= rows || !ok) break;
+              const float l0 = (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]), l1 = ml[N + r];
+              const float M = l1 != 0.f ? (l0 != 0.f ? fmaxf(m[r], ml[r]) : ml[r]) : m[r];
+              // a group without visible keys has l = 0 and an O^T that may not be set
+              const float f0 = l0 != 0.f ? ptx::ex2_approx(m[r] - M) : 0.f;
+              const float f1 = l1 != 0.f ? ptx::ex2_approx(ml[r] - M) : 0.f;
+              const float o = (l0 != 0.f ? __uint_as_float(w[r]) * f0 : 0.f) + (l1 != 0.f ? obuf[r * 128 + kk] * f1 : 0.f);
+              finish(r, o, M, (l0 != 0.f ? l0 * f0 : 0.f) + (l1 != 0.f ? l1 * f1 : 0.f));
+            }
+          }
         }
-        ptx::tc_fence_before();
       }
-      ptx::named_bar(2, 128);                               // the sums are read
+      ptx::tc_fence_before();
+      if constexpr (BYROW) ptx::named_bar(bar_g, 128);      // the sums are read
+      else ptx::named_bar(3, 256);                          // and group 1's half
       x += sg.cnt;
     }
   }

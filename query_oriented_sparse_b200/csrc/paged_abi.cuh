@@ -120,6 +120,23 @@ cudaError_t launch_stream_rows(StreamParams& p, const SeqTable& tab, int max_cta
   }
 }
 
+// Row-major [rows, cols] bf16 pool, rows a multiple of 8, as groups of eight rows and halves of
+// 64 columns: a box is box_rows rows whole, laid down as [group][half][8 rows][128 bytes].
+quoka_status make_map_groups(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows,
+                             const char* what) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return fail(QUOKA_ERR_CUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[4] = {64, 8, cols / 64, rows / 8};
+  const cuuint64_t strides[3] = {cols * 2, 128, cols * 16};
+  const cuuint32_t box[4] = {64, 8, (cuuint32_t)(cols / 64), box_rows / 8};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(QUOKA_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed: %d", what, (int)r);
+  return QUOKA_OK;
+}
+
 // bf16: one CTA per SM.
 template <int D, int N, bool kPaged>
 quoka_status launch_stream_tc(StreamParams& p, const SeqTable& tab, int max_ctas, const void* q, const void* k,
@@ -134,8 +151,13 @@ quoka_status launch_stream_tc(StreamParams& p, const SeqTable& tab, int max_ctas
   CUtensorMap qmap, kmap, vmap;
   quoka_status s;
   if ((s = make_map_bf16(&qmap, q, (uint64_t)p.batch * p.h_q, D, 64, N, "q")) != QUOKA_OK) return s;
-  if ((s = make_map_bf16(&kmap, k, rows, D, 64, box, "keys")) != QUOKA_OK) return s;
-  if ((s = make_map_bf16(&vmap, v, rows, D, 64, box, "values")) != QUOKA_OK) return s;
+  if (kPaged) {
+    if ((s = make_map_groups(&kmap, k, rows, D, box, "k_pages")) != QUOKA_OK) return s;
+    if ((s = make_map_groups(&vmap, v, rows, D, box, "v_pages")) != QUOKA_OK) return s;
+  } else {
+    if ((s = make_map_bf16(&kmap, k, rows, D, 64, box, "k_cache")) != QUOKA_OK) return s;
+    if ((s = make_map_bf16(&vmap, v, rows, D, 64, box, "v_cache")) != QUOKA_OK) return s;
+  }
   const int smem = Stc2Cfg<D, N>::smem(p.batch);
   cudaError_t e = ensure_smem(attn_stream_tc_kernel<D, N, kPaged>, smem);
   if (e != cudaSuccess) return cuda_fail(e, "attn_stream_tc smem");
@@ -169,9 +191,8 @@ quoka_status launch_stream(const Dims& d, const SeqTable& tab, StreamParams p, c
       return cuda_fail(e, "attn_stream launch");
     prof_mark(st, "attn_stream_kernel");
   }
-  const int jsmem = (2 * d.batch + 1 + std::min(p.ctas, w.max_unit_tiles) * d.G) * 4;
-  if ((e = ensure_smem(attn_stream_join_kernel<T, D, kPaged>, jsmem)) != cudaSuccess) return cuda_fail(e, "join smem");
-  attn_stream_join_kernel<T, D, kPaged><<<d.batch * d.h_kv, ASJ_THREADS, jsmem, st>>>(p, tab, reinterpret_cast<T*>(out));
+  const int jblocks = (d.batch * d.h_q + ASJ_ROWS - 1) / ASJ_ROWS;
+  attn_stream_join_kernel<T, D, kPaged><<<jblocks, ASJ_ROWS * 32, (2 * d.batch + 1) * 4, st>>>(p, tab, reinterpret_cast<T*>(out));
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attn_stream_join launch");
   prof_mark(st, "attn_stream_join_kernel");
   if (p.record) {
