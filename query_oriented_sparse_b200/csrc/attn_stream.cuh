@@ -18,6 +18,7 @@
 #pragma once
 #include "attn_decode.cuh"
 #include "kv_pages.cuh"
+#include "tc_ptx.cuh"
 
 namespace quoka {
 
@@ -162,6 +163,7 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
   using Cfg = AdcCfg<T, D>;
   constexpr int NW = Cfg::NW, ROW = Cfg::ROW, VPR = Cfg::VPR, EPV = Cfg::EPV, EPL = Cfg::EPL;
   extern __shared__ __align__(16) unsigned char smem[];
+  ptx::launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float* qs = reinterpret_cast<float*>(smem);              // [R][D], times scale * log2(e)
   float* mls = qs + R * D;                                 // [NW][R][2]
@@ -348,13 +350,16 @@ __device__ __forceinline__ int stream_slot(int c, int s, int ctas, int tiles) {
 }
 
 // One warp per output row (sequence, query head): out = sum_c o_c 2^(m_c - M) / sum_c l_c 2^(m_c - M)
-// over the CTAs that share its (sequence, KV head).
+// over the CTAs that share its (sequence, KV head).  Launched as a programmatic dependent: its
+// blocks work out their units while the streaming kernel still runs (8 us -> PDLFIG per step).
 template <typename T, int D, bool kPaged>
 __global__ void __launch_bounds__(ASJ_ROWS * 32)
 attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab,
                         T* __restrict__ out) {
   extern __shared__ int base[];                            // [batch + 1], lengths [batch]
+  ptx::launch_dependents();
   stream_bases<kPaged>(p, tab, base + p.batch + 1, base);
+  ptx::wait_dependency();                                  // in every block: what follows this grid relies on it
   const int tiles = base[p.batch] * p.h_kv, ctas = min(p.ctas, tiles);
   const int row = blockIdx.x * ASJ_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= p.batch * p.h_q) return;
@@ -420,6 +425,7 @@ attn_stream_record_kernel(const __grid_constant__ StreamParams p, const __grid_c
   extern __shared__ int base[];                            // [batch + 1], lengths [batch]
   const int* lens = base + p.batch + 1;
   stream_bases<true>(p, tab, base + p.batch + 1, base);
+  ptx::wait_dependency();
   const int tiles = base[p.batch] * p.h_kv;
   for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
     const StreamSeg sg = stream_seg_of(p, lens, base, x, x + 1);

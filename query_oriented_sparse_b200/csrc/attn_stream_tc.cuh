@@ -13,7 +13,7 @@
 // sum and O^T, joined at the end of a segment; for more rows, where a tile's exponentials
 // weigh more than its barriers, each takes half of the rows of every tile.
 //
-// Warp 0 loads: pages are copied box by box (a box is the largest power of two of rows that
+// Warps 0 and 11 load: pages are copied box by box (a box is the largest power of two of rows that
 // divides the page size, at most 128), only boxes with a visible key, and marks the boxes
 // whose page was bad.  A paged box is one copy: the tensor map splits rows into groups of
 // eight and their two 128-byte halves, so that the copy lays down whole swizzle atoms
@@ -27,11 +27,12 @@
 // selection.  P is rounded to bf16 for its MMA (the sums are taken before).
 #pragma once
 #include "tc_ptx.cuh"
+#include <climits>
 #include "attn_stream.cuh"
 
 namespace quoka {
 
-constexpr int STC2_THREADS = 352;         // warp 0 load, 1 S, 2-9 softmax, 10 P.V
+constexpr int STC2_THREADS = 448;         // warps 0 and 11 load Q and K, 12 and 13 V, 1 S, 2-9 softmax, 10 P.V
 constexpr float STC2_RESCALE_LOG2 = 8.0f;
 
 template <int D, int N>
@@ -98,6 +99,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   int* lens = base + p.batch + 1;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ptx::launch_dependents();               // the join's blocks may be placed as SMs fall free; they wait for this grid
   if (threadIdx.x == 0) {
     ptx::prefetch_tmap(&kmap);
     ptx::prefetch_tmap(&vmap);
@@ -130,14 +132,41 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   const int x0 = c < ctas ? stream_start(c, ctas, tiles) : 0, x1 = c < ctas ? stream_start(c + 1, ctas, tiles) : 0;
   auto seg_at = [&](int x) { return stream_seg_of(p, lens, base, x, x1); };
 
-  if (warp == 0) {
-    // ---------------- loads ----------------
-    const int nb = AST_TILE / box;                  // boxes per tile
+  if (warp == 0 || warp > 10) {
+    // ---------------- loads: Q and K, V; two warps each, which take the copies in turn (one
+    // warp issues a copy about every 60 ns) ----------------
+    const bool isv = warp > 11;
+    const int share = warp == 11 || warp == 13;
+    const bool lead = share == 0;                   // of the two: counts the tile's bytes
+    // The rows of 32 boxes (one per lane, several tiles) are looked up at a time, a batch ahead
+    // of their copies: a table entry comes from L2 or HBM.
+    const int nb = AST_TILE / box, tb = 32 / nb;    // boxes per tile, tiles per batch
+    int page = -1, off = 0;                         // next batch: this lane's page (contiguous: row), row in the pool
+    auto look = [&](int xb) {
+      page = -1;
+      off = 0;
+      const int x = xb + lane / nb;
+      if (x >= x1) return;
+      const StreamSeg sg = stream_seg_of(p, lens, base, x, x + 1);
+      const int k0 = sg.span.tile(sg.i0) * AST_TILE + (lane % nb) * box;
+      if (k0 >= sg.span.n || !(k0 < sg.span.ns || k0 + box > sg.span.lo)) return;
+      if constexpr (kPaged) {
+        const int pg = k0 / p.kv.page_size;
+        off = sg.g * p.kv.page_size + k0 - pg * p.kv.page_size;
+        page = __ldg(p.kv.block_table + (size_t)sg.b * p.kv.max_pages + pg);
+        if (page < 0) page = INT_MIN;               // (an entry that is not a page: -1 is a box that is not wanted)
+      } else {
+        page = (int)stream_row<false>(p, tab, sg.b, sg.g, k0);
+      }
+    };
     bool ok = true;
     int n = 0, sn = 0;                              // tiles, segments so far
+    int row = 0, bi0 = 0;                           // current batch: this lane's row; its tiles' first lane
+    uint32_t set = 0;
+    look(x0);
     for (int x = x0; x < x1 && ok; ++sn) {
       const StreamSeg sg = seg_at(x);
-      if (lane == 0) {
+      if (lane == 0 && warp == 0) {
         const int qb = sn % QB;
         ok = ptx::mbar_wait_sleep(&qempty[qb], ((uint32_t)(sn / QB) & 1u) ^ 1u);
         if (ok) {
@@ -150,44 +179,40 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       ok = __shfl_sync(0xffffffffu, ok, 0);
       for (int i = 0; i < sg.cnt && ok; ++i, ++n) {
         const int st = n % NST;
-        // lane i < nb: the pool row of box i, and whether it is loaded
-        const int k0 = sg.span.tile(sg.i0 + i) * AST_TILE + lane * box;
-        bool on = lane < nb && k0 < sg.span.n && (k0 < sg.span.ns || k0 + box > sg.span.lo);
-        int row = 0;
-        if (on) {
-          const long long rr = stream_row<kPaged>(p, tab, sg.b, sg.g, k0);
-          on = rr >= 0;
-          row = on ? (int)rr : 0;                   // pools and caches hold fewer than 2^31 rows
+        if (n % tb == 0) {                          // the next batch
+          bool on = page != -1;
+          if (kPaged && on && (page < 0 || page >= p.kv.num_pages)) {
+            if (warp == 0) flag_error(ERR_BAD_INDEX);
+            on = false;
+          }
+          // pools and caches hold fewer than 2^31 rows
+          row = on ? (kPaged ? page * (p.h_kv * p.kv.page_size) + off : page) : 0;
+          set = __ballot_sync(0xffffffffu, on);
+          look(x0 + n + tb);
         }
-        const uint32_t set = __ballot_sync(0xffffffffu, on);
+        bi0 = (n % tb) * nb;
+        const uint32_t mine = (set >> bi0) & (nb == 32 ? ~0u : (1u << nb) - 1u);
         if (lane == 0) ok = ptx::mbar_wait_sleep(&empty[st], ((uint32_t)(n / NST) & 1u) ^ 1u);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        if (lane == 0) {
-          const uint32_t bytes = (uint32_t)(__popc(set) * box * D * 2);
-          boxes[st] = set;
-          ptx::mbar_expect_tx(&kfull[st], bytes);
-          ptx::mbar_expect_tx(&vfull[st], bytes);
+        uint64_t* full = (isv ? vfull : kfull) + st;
+        if (lane == 0 && lead) {
+          if (!isv) boxes[st] = mine;
+          ptx::mbar_expect_tx(full, (uint32_t)(__popc(mine) * box * D * 2));
         }
         __syncwarp();
-        uint8_t* sV = sKV + st * Cfg::STAGE;
-        if constexpr (kPaged) {
-          // lane e < nb: K of box e; lane e + 16: its V
-          const int bi = lane & 15;
-          const int r = __shfl_sync(0xffffffffu, row, bi);
-          if (bi < nb && ((set >> bi) & 1u)) {
-            const bool isv = lane >= 16;
-            ptx::tma_load_4d(sV + (isv ? 0 : Cfg::T_BYTES) + bi * box * D * 2, isv ? &vmap : &kmap,
-                             isv ? &vfull[st] : &kfull[st], 0, 0, 0, r >> 3);
-          }
-        } else {
-          // one box: lane e < KB: half e of K; lane e + KB: of V
-          const int r = __shfl_sync(0xffffffffu, row, 0);
-          if (lane < 2 * KB && set) {
-            const bool isv = lane >= KB;
-            ptx::tma_load_2d(sV + (isv ? 0 : Cfg::T_BYTES) + (lane % KB) * 16384, isv ? &vmap : &kmap,
-                             isv ? &vfull[st] : &kfull[st], (lane % KB) * 64, r);
-          }
+        uint8_t* dst = sKV + st * Cfg::STAGE + (isv ? 0 : Cfg::T_BYTES);
+        const CUtensorMap* map = isv ? &vmap : &kmap;
+        const int e = 2 * lane + share;
+        if constexpr (kPaged) {                     // copy e: box e
+          const int r = __shfl_sync(0xffffffffu, row, bi0 + e % nb);
+          if (e < nb && ((mine >> e) & 1u))
+            ptx::tma_load_4d(dst + e * box * D * 2, map, full, 0, 0, 0, r >> 3);
+        } else {                                    // copy e: half e / nb of box e % nb
+          const int bi = e % nb, kb = e / nb;
+          const int r = __shfl_sync(0xffffffffu, row, bi0 + bi);
+          if (kb < KB && ((mine >> bi) & 1u))
+            ptx::tma_load_2d(dst + kb * 16384 + bi * box * 128, map, full, kb * 64, r);
         }
       }
       x += sg.cnt;
@@ -323,9 +348,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
           for (int r = 0; r < NR; ++r) {
             if (r >= rows) break;
-            float v = s[r];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            const float v = ptx::warp_max(s[r]);
             if (lane == (r & 31)) wmax[quarter * NR + r] = v;
           }
           ptx::named_bar(bar_g, 128);

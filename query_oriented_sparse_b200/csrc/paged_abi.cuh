@@ -91,6 +91,23 @@ StreamWs stream_ws(const Dims& d, long long max_keys, bool record) {
   return w;
 }
 
+// Launches a kernel that may start before the one ahead of it on the stream has finished (it
+// waits for it itself).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at = {};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
 template <typename T, int D, int R, bool kPaged>
 cudaError_t launch_stream_simt(const StreamParams& p, const SeqTable& tab, const void* q, const void* k,
                                const void* v, void* out, cudaStream_t st) {
@@ -142,7 +159,9 @@ template <int D, int N, bool kPaged>
 quoka_status launch_stream_tc(StreamParams& p, const SeqTable& tab, int max_ctas, const void* q, const void* k,
                               const void* v, void* out, cudaStream_t st) {
   p.ctas = std::min(max_ctas, sm_count());
-  int box = AST_TILE;                    // rows per copy: a power of two that divides the pages
+  // Rows per copy: a power of two that divides the pages; over the contiguous cache 32, since the
+  // first tokens and the window's ends leave most of their tiles' rows unread
+  int box = kPaged ? AST_TILE : 32;
   uint64_t rows = (uint64_t)p.h_kv * p.kv.rows_per_head;
   if (kPaged) {
     while (p.kv.page_size % box) box /= 2;
@@ -192,13 +211,14 @@ quoka_status launch_stream(const Dims& d, const SeqTable& tab, StreamParams p, c
     prof_mark(st, "attn_stream_kernel");
   }
   const int jblocks = (d.batch * d.h_q + ASJ_ROWS - 1) / ASJ_ROWS;
-  attn_stream_join_kernel<T, D, kPaged><<<jblocks, ASJ_ROWS * 32, (2 * d.batch + 1) * 4, st>>>(p, tab, reinterpret_cast<T*>(out));
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attn_stream_join launch");
+  if ((e = launch_dependent(attn_stream_join_kernel<T, D, kPaged>, jblocks, ASJ_ROWS * 32, (2 * d.batch + 1) * 4, st, p,
+                            tab, reinterpret_cast<T*>(out))) != cudaSuccess)
+    return cuda_fail(e, "attn_stream_join launch");
   prof_mark(st, "attn_stream_join_kernel");
   if (p.record) {
     const int grid = (int)std::min<long long>(w.max_tiles, (long long)sm_count() * 16);
-    attn_stream_record_kernel<<<grid, AST_TILE, (2 * d.batch + 1) * 4, st>>>(p, tab);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attn_stream_record launch");
+    if ((e = launch_dependent(attn_stream_record_kernel, grid, AST_TILE, (2 * d.batch + 1) * 4, st, p, tab)) != cudaSuccess)
+      return cuda_fail(e, "attn_stream_record launch");
     prof_mark(st, "attn_stream_record_kernel");
   }
   return QUOKA_OK;
