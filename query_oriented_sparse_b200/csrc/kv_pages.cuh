@@ -12,6 +12,7 @@
 //   evict_copy_kernel    the kept rows and their records, in order, into other pages.
 #pragma once
 #include "cluster_select.cuh"
+#include "tc_ptx.cuh"
 
 namespace quoka {
 
@@ -98,6 +99,7 @@ __device__ __forceinline__ EvictSplit evict_split(const KvView& kv, const int32_
 
 constexpr int EVS_THREADS = 512;
 constexpr int EVS_MAX_CS = 16;
+constexpr int EVS_UNROLL = 4;
 constexpr int EVS_STAGE_KEYS = 49152;          // candidate keys a CTA stages (192 KB)
 
 // One cluster of CS CTAs per (sequence, KV head).
@@ -109,6 +111,7 @@ evict_select_kernel(const float* __restrict__ record, const KvView kv, const int
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ SelectSmem sm;
   extern __shared__ uint32_t staged[];
+  ptx::launch_dependents();
 
   const int rank = (int)cluster.block_rank();
   const int head = blockIdx.x / CS;
@@ -130,11 +133,30 @@ evict_select_kernel(const float* __restrict__ record, const KvView kv, const int
   const int cand = s.n - s.first - s.last;
   const int per = (cand + CS - 1) / CS;
   const int lo = min(cand, rank * per), hi = min(cand, lo + per);
-  // the slice's weights as ordered keys; NaN ranks with -inf, behind every number
-  for (int j = lo + threadIdx.x; j < hi; j += blockDim.x) {
-    const long long row = paged_row(kv, b, g, h_kv, s.first + j);
-    const float w = row < 0 ? -INFINITY : __ldg(record + row);
-    staged[j - lo] = float_to_ordered(w == w ? w : -INFINITY);
+  // The slice's weights as ordered keys; NaN ranks with -inf, behind every number.  Positions
+  // 4 i .. 4 i + 3 share a page: one table entry and one 16-byte load for four keys, and
+  // EVS_UNROLL such groups in flight per thread.
+  const int p0 = s.first + lo, p1 = s.first + hi;
+  for (int i0 = p0 / 4 + threadIdx.x; 4 * i0 < p1; i0 += EVS_UNROLL * blockDim.x) {
+    long long row[EVS_UNROLL];
+#pragma unroll
+    for (int u = 0; u < EVS_UNROLL; ++u) {
+      const int j = 4 * (i0 + u * (int)blockDim.x);
+      row[u] = j < p1 ? paged_row(kv, b, g, h_kv, j) : -1;
+    }
+    float4 w[EVS_UNROLL];
+#pragma unroll
+    for (int u = 0; u < EVS_UNROLL; ++u)
+      w[u] = row[u] < 0 ? make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY)
+                        : __ldg(reinterpret_cast<const float4*>(record + row[u]));
+#pragma unroll
+    for (int u = 0; u < EVS_UNROLL; ++u) {
+      const int j = 4 * (i0 + u * (int)blockDim.x);
+      const float x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (j + e >= p0 && j + e < p1) staged[j + e - p0] = float_to_ordered(x[e] == x[e] ? x[e] : -INFINITY);
+    }
   }
   __syncthreads();
   auto key_at = [&](int j) { return staged[j - lo]; };
@@ -146,23 +168,56 @@ evict_select_kernel(const float* __restrict__ record, const KvView kv, const int
   cluster_wait();                              // peers' last reads of this CTA's histograms
 }
 
-// Kept row i of (b, g), position idx[i], to position i of dst (its own table).
-__global__ void __launch_bounds__(PAGED_THREADS)
+// Kept row i of (b, g), position idx[i], to position i of dst (its own table).  A warp takes 32
+// rows: lane l looks up where row l lies and goes, then the rows' 16-byte vectors are copied
+// with EVC_UNROLL loads each of K and V in flight per lane.  Bound by the rows' bytes; with a
+// lookup per vector instead of per row and one load in flight it took 121 us instead of
+// EVCFIG for the 32-sequence case (507 MB).
+constexpr int EVC_WARPS = 8;
+constexpr int EVC_UNROLL = 8;
+
+template <int VPR>                             // 16-byte vectors per row
+__global__ void __launch_bounds__(EVC_WARPS * 32)
 evict_copy_kernel(uint4* __restrict__ k, uint4* __restrict__ v, float* __restrict__ record, const KvView kv,
                   const KvView dst, const int32_t* __restrict__ idx, const int32_t* __restrict__ new_len,
-                  int h_kv, int b_max, int vpr) {
+                  int h_kv, int b_max) {
+  ptx::wait_dependency();
   const int head = blockIdx.x;
   const int b = head / h_kv, g = head - b * h_kv;
+  const int lane = threadIdx.x & 31;
   const int kept = new_len[b];
-  const int total = kept * vpr;
-  for (int e = blockIdx.y * blockDim.x + threadIdx.x; e < total; e += gridDim.y * blockDim.x) {
-    const int i = e / vpr, vec = e - i * vpr;
-    const long long from = paged_row(kv, b, g, h_kv, idx[(size_t)head * b_max + i]);
-    const long long to = paged_row(dst, b, g, h_kv, i);
-    if (from < 0 || to < 0) continue;
-    k[to * vpr + vec] = k[from * vpr + vec];
-    v[to * vpr + vec] = v[from * vpr + vec];
-    if (vec == 0) record[to] = record[from];
+  const int i0 = (blockIdx.y * EVC_WARPS + (threadIdx.x >> 5)) * 32;
+  if (i0 >= kept) return;
+  int from = -1, to = -1;                      // pools hold fewer than 2^31 rows
+  if (i0 + lane < kept) {
+    from = (int)paged_row(kv, b, g, h_kv, idx[(size_t)head * b_max + i0 + lane]);
+    to = (int)paged_row(dst, b, g, h_kv, i0 + lane);
+    if (from < 0) to = -1;
+    if (to >= 0) record[to] = record[from];
+  }
+  // vector e of the 32 rows: row e / VPR
+#pragma unroll 1
+  for (int e0 = 0; e0 < VPR; e0 += EVC_UNROLL) {
+    uint4 kx[EVC_UNROLL], vx[EVC_UNROLL];
+    int at[EVC_UNROLL];
+#pragma unroll
+    for (int u = 0; u < EVC_UNROLL; ++u) {
+      const int e = (e0 + u) * 32 + lane, vec = e % VPR;
+      const int f = __shfl_sync(0xffffffffu, from, e / VPR);
+      at[u] = __shfl_sync(0xffffffffu, to, e / VPR);
+      if (at[u] >= 0) {
+        kx[u] = __ldcs(k + (size_t)f * VPR + vec);
+        vx[u] = __ldcs(v + (size_t)f * VPR + vec);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < EVC_UNROLL; ++u) {
+      const int vec = ((e0 + u) * 32 + lane) % VPR;
+      if (at[u] >= 0) {
+        __stcs(k + (size_t)at[u] * VPR + vec, kx[u]);
+        __stcs(v + (size_t)at[u] * VPR + vec, vx[u]);
+      }
+    }
   }
 }
 

@@ -94,9 +94,9 @@ StreamWs stream_ws(const Dims& d, long long max_keys, bool record) {
 // Launches a kernel that may start before the one ahead of it on the stream has finished (it
 // waits for it itself).
 template <typename... P, typename... A>
-cudaError_t launch_dependent(void (*kern)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
+cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block, size_t smem, cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -536,13 +536,17 @@ quoka_status paged_evict(const quoka_paged_shape* shape, void* k_pages, void* v_
     }
     if (e != cudaSuccess) return cuda_fail(e, "evict_select launch");
     prof_mark(st, "evict_select_kernel");
-    const int vpr = p.d.D * p.d.esz / 16;
-    const int gy = (int)std::max<long long>(1, std::min<long long>(((long long)std::min(b_max, max_len) * vpr + PAGED_THREADS - 1) / PAGED_THREADS,
-                                                                   ((long long)sm_count() * 16 + nrows - 1) / nrows));
-    evict_copy_kernel<<<dim3(nrows, gy), PAGED_THREADS, 0, st>>>(
-        reinterpret_cast<uint4*>(k_pages), reinterpret_cast<uint4*>(v_pages), record, kv, dst, idx_out, new_len, p.d.h_kv,
-        b_max, vpr);
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "evict_copy launch");
+    const dim3 cgrid(nrows, (std::min(b_max, max_len) + EVC_WARPS * 32 - 1) / (EVC_WARPS * 32));
+    auto copy = [&](auto kern) {
+      return launch_dependent(kern, cgrid, EVC_WARPS * 32, 0, st, reinterpret_cast<uint4*>(k_pages),
+                              reinterpret_cast<uint4*>(v_pages), record, kv, dst, idx_out, new_len, p.d.h_kv, b_max);
+    };
+    switch (p.d.D * p.d.esz / 16) {
+      case 8: e = copy(evict_copy_kernel<8>); break;
+      case 16: e = copy(evict_copy_kernel<16>); break;
+      default: e = copy(evict_copy_kernel<32>); break;
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "evict_copy launch");
     prof_mark(st, "evict_copy_kernel");
     return QUOKA_OK;
   });
