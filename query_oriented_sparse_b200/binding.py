@@ -145,7 +145,13 @@ def _host_i32(xs: Sequence[int]):
     return (ctypes.c_int32 * len(xs))(*[int(x) for x in xs])
 
 
+# the current stream's handle without a Stream object around it, where torch has that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream: Optional[torch.cuda.Stream]) -> int:
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
     s = stream if stream is not None else torch.cuda.current_stream()
     return s.cuda_stream
 
@@ -347,6 +353,9 @@ def quoka_prefill(q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
     return out
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
     """Context of a call on tensors of `dev`: that device current, and `stream` (when given)
     the stream on which the call's outputs and scratch are allocated."""
@@ -356,18 +365,23 @@ def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
         return torch.cuda.stream(stream)
     if dev.type == "cuda" and dev.index != torch.cuda.current_device():
         return torch.cuda.device(dev)
-    return contextlib.nullcontext()
+    return _HERE_AND_NOW
 
 
 def _need(name: str, t: torch.Tensor, shape: Tuple[int, ...], dtype: torch.dtype, dev: torch.device) -> None:
+    if t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return
     if t.shape != shape:
         raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if t.dtype != dtype:
         raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} is {t.dtype}, not {dtype}")
     if t.device != dev:
         raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} is on {t.device}, not {dev}")
-    if not t.is_contiguous():
-        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} must be contiguous")
+    raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} must be contiguous")
+
+
+def _adr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(workspace: Optional[torch.Tensor], n: int, dev: torch.device):
@@ -416,10 +430,13 @@ def window_chunk_attn(q_chunk: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         n = window_workspace_size(shape, max(prefix_len), window) if workspace is None else 0
         workspace, ws_bytes = _scratch(workspace, n, dev)
         _check(lib().window_chunk_attn(
-            ctypes.byref(shape), _ptr(q_chunk), _ptr(k_cache), _ptr(v_cache), _host_i64(kv_off),
-            _host_i32(prefix_len), int(window), int(n_sink), _ptr(out), _ptr(workspace), ws_bytes,
-            ctypes.c_void_p(_stream(stream))))
+            ctypes.byref(shape), _adr(q_chunk), _adr(k_cache), _adr(v_cache), _host_i64(kv_off),
+            _host_i32(prefix_len), int(window), int(n_sink), _adr(out), _adr(workspace), ws_bytes,
+            _stream(stream)))
     return out
+
+
+_DTYPES = {torch.float32: QUOKA_F32, torch.bfloat16: QUOKA_BF16}
 
 
 def paged_shape(h_q: int, k_pages: torch.Tensor, block_table: torch.Tensor) -> QuokaPagedShape:
@@ -427,8 +444,10 @@ def paged_shape(h_q: int, k_pages: torch.Tensor, block_table: torch.Tensor) -> Q
     [batch, max_pages]."""
     num_pages, h_kv, page, d = _dims(k_pages, "k_pages", 4)
     batch, max_pages = _dims(block_table, "block_table", 2)
-    one = make_shape(batch, h_q, h_kv, d, 1, k_pages.dtype)
-    return QuokaPagedShape(batch, h_q, h_kv, d, one.dtype, page, num_pages, max_pages)
+    dt = _DTYPES.get(k_pages.dtype)
+    if dt is None:
+        raise QuokaError(QUOKA_ERR_UNSUPPORTED, f"dtype {k_pages.dtype}")
+    return QuokaPagedShape(batch, h_q, h_kv, d, dt, page, num_pages, max_pages)
 
 
 def _need_pools(k_pages, v_pages, record, block_table, dev) -> None:
@@ -457,9 +476,9 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor
         _need("n_new", n_new, (shape.batch,), torch.int32, dev)
     with _on(dev, stream):
         _check(lib().paged_append(
-            ctypes.byref(shape), _ptr(k_new), _ptr(v_new), n, _ptr(k_pages), _ptr(v_pages),
-            _ptr(weight_pages), _ptr(block_table), _ptr(start), _ptr(n_new),
-            ctypes.c_void_p(_stream(stream))))
+            ctypes.byref(shape), _adr(k_new), _adr(v_new), n, _adr(k_pages), _adr(v_pages),
+            _adr(weight_pages), _adr(block_table), _adr(start), _adr(n_new),
+            _stream(stream)))
 
 
 def paged_decode_workspace_size(shape: QuokaPagedShape, max_len: int, with_record: bool) -> int:
@@ -491,9 +510,9 @@ def paged_decode_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
             workspace, paged_decode_workspace_size(shape, max_len, weight_pages is not None)
             if workspace is None else 0, dev)
         _check(lib().paged_decode_attn(
-            ctypes.byref(shape), _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(block_table), _ptr(seq_len),
-            int(max_len), int(max_len if window is None else window), int(n_sink), _ptr(weight_pages),
-            _ptr(out), _ptr(workspace), ws_bytes, ctypes.c_void_p(_stream(stream))))
+            ctypes.byref(shape), _adr(q), _adr(k_pages), _adr(v_pages), _adr(block_table), _adr(seq_len),
+            int(max_len), int(max_len if window is None else window), int(n_sink), _adr(weight_pages),
+            _adr(out), _adr(workspace), ws_bytes, _stream(stream)))
     return out
 
 
@@ -522,9 +541,9 @@ def paged_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weight_pages: torc
         else:
             _need("new_len", new_len, (shape.batch,), torch.int32, dev)
         _check(lib().paged_evict(
-            ctypes.byref(shape), _ptr(k_pages), _ptr(v_pages), _ptr(weight_pages), _ptr(block_table),
-            _ptr(seq_len), int(max_len), _ptr(budget), int(b_max), int(n_sink), int(n_recent),
-            _ptr(dst_table), dst_pages, _ptr(idx_out), _ptr(new_len), ctypes.c_void_p(_stream(stream))))
+            ctypes.byref(shape), _adr(k_pages), _adr(v_pages), _adr(weight_pages), _adr(block_table),
+            _adr(seq_len), int(max_len), _adr(budget), int(b_max), int(n_sink), int(n_recent),
+            _adr(dst_table), dst_pages, _adr(idx_out), _adr(new_len), _stream(stream)))
     return idx_out, new_len
 
 

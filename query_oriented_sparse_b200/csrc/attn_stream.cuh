@@ -10,7 +10,8 @@
 // device, so a captured graph serves growing sequences.  A (sequence, KV head) that one
 // CTA holds whole is finished there; one that several share leaves at most one partial
 // (running maximum, sum and output, fp32) per CTA, two slots in all, and the join kernel
-// merges them.  With a weight record, the logits are kept (fp32, base 2) and the record
+// merges them.  Where the sequences are short (four tiles at most), a CTA takes a (sequence,
+// KV head) whole instead, and there is nothing to join: one launch.  With a weight record, the logits are kept (fp32, base 2) and the record
 // kernel adds each key's softmax weight, summed over the group's heads, once the join has
 // the row's maximum and sum.
 //
@@ -53,6 +54,8 @@ struct StreamParams {
   int window, n_sink;
   float scale_log2;                       // log2(e) / sqrt(d)
   int ctas;                               // N at most (the tiles, when they are fewer)
+  int by_unit;                            // CTA c takes the whole (sequence, KV head) c: nothing to join
+  int own_record;                         // and adds its keys' weights itself
   float* part;                            // [2 N][G][D] partial outputs
   float* part_ml;                         // [2 N][G][2] their running maximum (base 2) and sum
   float* unit_ml;                         // [batch * h_kv][G][2] maximum and 1 / sum (with a record)
@@ -111,6 +114,20 @@ __device__ __forceinline__ int stream_seq(const int* base, int batch, int h_kv, 
   return lo;
 }
 
+// Tiles [x0, x1) of CTA c.
+__device__ __forceinline__ void stream_share(const StreamParams& p, const int* base, int c, int* x0, int* x1) {
+  const int tiles = base[p.batch] * p.h_kv;
+  if (p.by_unit) {
+    const int b = c / p.h_kv, nt = base[b + 1] - base[b];
+    *x0 = base[b] * p.h_kv + (c - b * p.h_kv) * nt;
+    *x1 = *x0 + nt;
+    return;
+  }
+  const int ctas = min(p.ctas, tiles);                     // every share holds a tile at least
+  *x0 = c < ctas ? stream_start(c, ctas, tiles) : 0;
+  *x1 = c < ctas ? stream_start(c + 1, ctas, tiles) : 0;
+}
+
 // A run of tiles of one (sequence, KV head) inside a CTA's share.
 struct StreamSeg {
   int b, g, unit, i0, cnt;                // tiles i0 .. i0 + cnt - 1 of the unit's nt
@@ -136,6 +153,17 @@ template <bool kPaged>
 __device__ __forceinline__ long long stream_row(const StreamParams& p, const SeqTable& tab, int b, int g, int j) {
   if constexpr (kPaged) return paged_row(p.kv, b, g, p.h_kv, j);
   else return (long long)g * p.kv.rows_per_head + tab.kv_off[b] + j;
+}
+
+// record[key] += sum over the group's heads of 2^(s - M) / L for key j of segment sg, whose logits
+// lie at lg.
+__device__ __forceinline__ void stream_record_key(const StreamParams& p, const StreamSeg& sg, int j, const float* lg) {
+  if (!sg.span.visible(j)) return;
+  const float* ml = p.unit_ml + (size_t)sg.unit * p.G * 2;
+  float w = 0.f;
+  for (int r = 0; r < p.G; ++r) w += exp2f(lg[r] - ml[2 * r]) * ml[2 * r + 1];
+  const long long row = paged_row(p.kv, sg.b, sg.g, p.h_kv, j);
+  if (row >= 0) atomicAdd(p.record + row, w);
 }
 
 // 16-byte asynchronous copy, or 16 zero bytes when `on` is false (nothing is read then).
@@ -174,12 +202,10 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
   int* lens = base + p.batch + 1;
   stream_bases<kPaged>(p, tab, lens, base);
 
-  const int tiles = base[p.batch] * p.h_kv;
-  const int ctas = min(p.ctas, tiles);                     // every share holds a tile at least
   const int c = blockIdx.x, r0 = blockIdx.y * R;
-  if (c >= ctas) return;
   const int rows = min(R, p.G - r0);
-  const int x0 = stream_start(c, ctas, tiles), x1 = stream_start(c + 1, ctas, tiles);
+  int x0, x1;
+  stream_share(p, base, c, &x0, &x1);
   for (int x = x0; x < x1;) {
     const StreamSeg sg = stream_seg_of(p, lens, base, x, x1);
     for (int e = threadIdx.x; e < R * D; e += blockDim.x) {
@@ -336,7 +362,11 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         }
       }
     }
-    __syncthreads();                                       // qs, mls and the stages are free
+    __syncthreads();                                       // qs, mls and the stages are free; unit_ml is there
+    if (kPaged && p.own_record)
+      for (int e = threadIdx.x; e < sg.cnt * AST_TILE; e += blockDim.x)
+        stream_record_key(p, sg, sg.span.tile(sg.i0 + e / AST_TILE) * AST_TILE + e % AST_TILE,
+                          p.logits + ((size_t)x * AST_TILE + e) * p.G);
     x += sg.cnt;
   }
 }
@@ -360,6 +390,7 @@ attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_con
   ptx::launch_dependents();
   stream_bases<kPaged>(p, tab, base + p.batch + 1, base);
   ptx::wait_dependency();                                  // in every block: what follows this grid relies on it
+  if (p.by_unit) return;                                   // nothing to join
   const int tiles = base[p.batch] * p.h_kv, ctas = min(p.ctas, tiles);
   const int row = blockIdx.x * ASJ_ROWS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (row >= p.batch * p.h_q) return;
@@ -418,7 +449,7 @@ attn_stream_join_kernel(const __grid_constant__ StreamParams p, const __grid_con
   for (int e = 0; e < E; ++e) out[(size_t)row * D + lane * E + e] = from_f32<T>(o[e] * inv);
 }
 
-// record[key] += sum over the group's heads of 2^(s - M) / L.  One thread per key of a tile.
+// One thread per key of a tile.
 // The add is a reduction in memory, so a page that two sequences share gets both sums.
 __global__ void __launch_bounds__(AST_TILE)
 attn_stream_record_kernel(const __grid_constant__ StreamParams p, const __grid_constant__ SeqTable tab) {
@@ -429,14 +460,8 @@ attn_stream_record_kernel(const __grid_constant__ StreamParams p, const __grid_c
   const int tiles = base[p.batch] * p.h_kv;
   for (int x = blockIdx.x; x < tiles; x += gridDim.x) {
     const StreamSeg sg = stream_seg_of(p, lens, base, x, x + 1);
-    const int j = sg.span.tile(sg.i0) * AST_TILE + threadIdx.x;
-    if (!sg.span.visible(j)) continue;
-    const float* lg = p.logits + ((size_t)x * AST_TILE + threadIdx.x) * p.G;
-    const float* ml = p.unit_ml + (size_t)sg.unit * p.G * 2;
-    float w = 0.f;
-    for (int r = 0; r < p.G; ++r) w += exp2f(lg[r] - ml[2 * r]) * ml[2 * r + 1];
-    const long long row = paged_row(p.kv, sg.b, sg.g, p.h_kv, j);
-    if (row >= 0) atomicAdd(p.record + row, w);
+    stream_record_key(p, sg, sg.span.tile(sg.i0) * AST_TILE + threadIdx.x,
+                      p.logits + ((size_t)x * AST_TILE + threadIdx.x) * p.G);
   }
 }
 

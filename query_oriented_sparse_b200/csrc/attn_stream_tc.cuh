@@ -126,10 +126,9 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  const int tiles = base[p.batch] * p.h_kv;
-  const int ctas = min(p.ctas, tiles);
   const int c = blockIdx.x;
-  const int x0 = c < ctas ? stream_start(c, ctas, tiles) : 0, x1 = c < ctas ? stream_start(c + 1, ctas, tiles) : 0;
+  int x0, x1;
+  stream_share(p, base, c, &x0, &x1);
   auto seg_at = [&](int x) { return stream_seg_of(p, lens, base, x, x1); };
 
   if (warp == 0 || warp > 10) {
@@ -485,8 +484,11 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
       }
       ptx::tc_fence_before();
-      if constexpr (BYROW) ptx::named_bar(bar_g, 128);      // the sums are read
-      else ptx::named_bar(3, 256);                          // and group 1's half
+      ptx::named_bar(3, 256);                               // the sums are read, and group 1's half
+      if (kPaged && p.own_record && ok)                     // (unit_ml and the logits are this CTA's own)
+        for (int e = threadIdx.x - 64; e < sg.cnt * AST_TILE; e += 256)
+          stream_record_key(p, sg, sg.span.tile(sg.i0 + e / AST_TILE) * AST_TILE + e % AST_TILE,
+                            p.logits + ((size_t)x * AST_TILE + e) * p.G);
       x += sg.cnt;
     }
   }

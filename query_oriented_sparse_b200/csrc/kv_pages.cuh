@@ -99,6 +99,7 @@ __device__ __forceinline__ EvictSplit evict_split(const KvView& kv, const int32_
 
 constexpr int EVS_THREADS = 512;
 constexpr int EVS_MAX_CS = 16;
+constexpr int EVS_SHARE_KEYS = 24576;          // staged keys up to which two CTAs share an SM
 constexpr int EVS_UNROLL = 4;
 constexpr int EVS_STAGE_KEYS = 49152;          // candidate keys a CTA stages (192 KB)
 
@@ -111,7 +112,6 @@ evict_select_kernel(const float* __restrict__ record, const KvView kv, const int
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ SelectSmem sm;
   extern __shared__ uint32_t staged[];
-  ptx::launch_dependents();
 
   const int rank = (int)cluster.block_rank();
   const int head = blockIdx.x / CS;

@@ -63,6 +63,7 @@ SeqTable empty_table() {
 }
 
 // ---- one new token per sequence: the streaming attention ---------------------------------
+constexpr int STREAM_UNIT_TILES = 4;   // tiles of a sequence up to which a CTA takes a unit whole
 constexpr int STREAM_MAX_CTAS = 592;   // CTAs of the streaming kernels at most (their partials' space)
 
 struct StreamWs {
@@ -127,7 +128,7 @@ cudaError_t launch_stream_rows(StreamParams& p, const SeqTable& tab, int max_cta
   int r = 1;
   while (r < std::min(p.G, 16)) r *= 2;
   const int per_sm = std::max(1, std::min(4, 230000 / (ast_smem_bytes<T, D, 16>(p.batch) + 1024)));
-  p.ctas = std::min(max_ctas, sm_count() * per_sm);
+  if (!p.by_unit) p.ctas = std::min(max_ctas, sm_count() * per_sm);
   switch (r) {
     case 1: return launch_stream_simt<T, D, 1, kPaged>(p, tab, q, k, v, out, st);
     case 2: return launch_stream_simt<T, D, 2, kPaged>(p, tab, q, k, v, out, st);
@@ -154,11 +155,11 @@ quoka_status make_map_groups(CUtensorMap* m, const void* base, uint64_t rows, ui
   return QUOKA_OK;
 }
 
-// bf16: one CTA per SM.
+// bf16: one CTA per SM (or per unit).
 template <int D, int N, bool kPaged>
 quoka_status launch_stream_tc(StreamParams& p, const SeqTable& tab, int max_ctas, const void* q, const void* k,
                               const void* v, void* out, cudaStream_t st) {
-  p.ctas = std::min(max_ctas, sm_count());
+  if (!p.by_unit) p.ctas = std::min(max_ctas, sm_count());
   // Rows per copy: a power of two that divides the pages; over the contiguous cache 32, since the
   // first tokens and the window's ends leave most of their tiles' rows unread
   int box = kPaged ? AST_TILE : 32;
@@ -199,6 +200,12 @@ quoka_status launch_stream(const Dims& d, const SeqTable& tab, StreamParams p, c
   p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
   p.unit_ml = reinterpret_cast<float*>(ws + w.unit_ml);
   p.logits = p.record ? reinterpret_cast<float*>(ws + w.logits) : nullptr;
+  // Sequences of up to STREAM_UNIT_TILES tiles: a (sequence, KV head) per CTA and one launch, while
+  // these CTAs are no more than the SMs (512 sequences and heads of 300 keys: 44 us against 40)
+  p.by_unit = w.max_unit_tiles - 2 <= STREAM_UNIT_TILES && d.batch * d.h_kv <= sm_count();
+  if (p.by_unit) p.ctas = d.batch * d.h_kv;
+  // (fp32 with more than 16 heads to a group splits them over CTAs: their sums meet in the kernel)
+  p.own_record = p.record && p.by_unit && (sizeof(T) == 2 || d.G <= 16);
   cudaError_t e;
   if constexpr (sizeof(T) == 2) {
     const quoka_status s = d.G <= 16   ? launch_stream_tc<D, 16, kPaged>(p, tab, w.ctas, q, k, v, out, st)
@@ -210,6 +217,7 @@ quoka_status launch_stream(const Dims& d, const SeqTable& tab, StreamParams p, c
       return cuda_fail(e, "attn_stream launch");
     prof_mark(st, "attn_stream_kernel");
   }
+  if (p.by_unit && (!p.record || p.own_record)) return QUOKA_OK;
   const int jblocks = (d.batch * d.h_q + ASJ_ROWS - 1) / ASJ_ROWS;
   if ((e = launch_dependent(attn_stream_join_kernel<T, D, kPaged>, jblocks, ASJ_ROWS * 32, (2 * d.batch + 1) * 4, st, p,
                             tab, reinterpret_cast<T*>(out))) != cudaSuccess)
@@ -518,6 +526,8 @@ quoka_status paged_evict(const quoka_paged_shape* shape, void* k_pages, void* v_
     int cs = EVS_MAX_CS;
     while (cs > 1 && (long long)nrows * cs > (long long)sm_count() && (max_len + cs / 2 - 1) / (cs / 2) <= EVS_STAGE_KEYS)
       cs /= 2;
+    // slices so long that a CTA fills an SM: more and shorter ones, while they fit the SMs together
+    while (cs < EVS_MAX_CS && (max_len + cs - 1) / cs > EVS_SHARE_KEYS && (long long)nrows * cs * 2 <= 4LL * sm_count()) cs *= 2;
     const int smem = std::max((max_len + cs - 1) / cs, 1) * 4;
     auto launch = [&](auto kern, int csz) -> cudaError_t {
       cudaError_t err = ensure_smem(kern, smem);
