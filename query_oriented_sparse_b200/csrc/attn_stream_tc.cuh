@@ -32,11 +32,14 @@
 
 namespace quoka {
 
-constexpr int STC2_THREADS = 448;         // warps 0 and 11 load Q and K, 12 and 13 V, 1 S, 2-9 softmax, 10 P.V
+// Warps: 0 loads Q and K, 1 issues S, 2-9 softmax, 10 P.V; for N = 16, 11 loads K with warp 0, 12 and
+// 13 V; for more rows, whose softmax needs the registers, 11 loads V.
 constexpr float STC2_RESCALE_LOG2 = 8.0f;
 
 template <int D, int N>
 struct Stc2Cfg {
+  static constexpr int LW = N == 16 ? 2 : 1;        // loading warps per operand
+  static constexpr int THREADS = N == 16 ? 448 : 384;
   static constexpr int KB = D / 64;                 // 128-byte blocks per row
   static constexpr int T_BYTES = AST_TILE * D * 2;  // one K or V tile
   static constexpr int STAGE = 2 * T_BYTES;         // V, then K
@@ -69,7 +72,7 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool v) {
 }
 
 template <int D, int N, bool kPaged>
-__global__ void __launch_bounds__(STC2_THREADS, 1)
+__global__ void __launch_bounds__(Stc2Cfg<D, N>::THREADS, 1)
 attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                       const __grid_constant__ CUtensorMap vmap, const __grid_constant__ StreamParams p,
                       const __grid_constant__ SeqTable tab, int box /* rows per TMA box */, __nv_bfloat16* __restrict__ out) {
@@ -118,7 +121,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
     ptx::tmem_alloc(tmem_slot, Cfg::TMEM);
     ptx::tmem_relinquish();
   }
-  for (int b = threadIdx.x; b < p.batch; b += STC2_THREADS) lens[b] = stream_len<kPaged>(p, tab, b);
+  for (int b = threadIdx.x; b < p.batch; b += Cfg::THREADS) lens[b] = stream_len<kPaged>(p, tab, b);
   __syncthreads();
   stream_bases_of(p, lens, base);
   ptx::tc_fence_before();
@@ -131,11 +134,12 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
   stream_share(p, base, c, &x0, &x1);
   auto seg_at = [&](int x) { return stream_seg_of(p, lens, base, x, x1); };
 
+  constexpr int LW = Cfg::LW;
   if (warp == 0 || warp > 10) {
-    // ---------------- loads: Q and K, V; two warps each, which take the copies in turn (one
-    // warp issues a copy about every 60 ns) ----------------
-    const bool isv = warp > 11;
-    const int share = warp == 11 || warp == 13;
+    // ---------------- loads: Q and K, V (two warps take an operand's copies in turn: one issues a
+    // copy about every 60 ns) ----------------
+    const bool isv = warp >= 10 + LW;
+    const int share = LW == 2 && (warp == 11 || warp == 13);
     const bool lead = share == 0;                   // of the two: counts the tile's bytes
     // The rows of 32 boxes (one per lane, several tiles) are looked up at a time, a batch ahead
     // of their copies: a table entry comes from L2 or HBM.
@@ -202,7 +206,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         __syncwarp();
         uint8_t* dst = sKV + st * Cfg::STAGE + (isv ? 0 : Cfg::T_BYTES);
         const CUtensorMap* map = isv ? &vmap : &kmap;
-        const int e = 2 * lane + share;
+        const int e = LW * lane + share;
         if constexpr (kPaged) {                     // copy e: box e
           const int r = __shfl_sync(0xffffffffu, row, bi0 + e % nb);
           if (e < nb && ((mine >> e) & 1u))

@@ -181,7 +181,7 @@ quoka_status launch_stream_tc(StreamParams& p, const SeqTable& tab, int max_ctas
   const int smem = Stc2Cfg<D, N>::smem(p.batch);
   cudaError_t e = ensure_smem(attn_stream_tc_kernel<D, N, kPaged>, smem);
   if (e != cudaSuccess) return cuda_fail(e, "attn_stream_tc smem");
-  attn_stream_tc_kernel<D, N, kPaged><<<p.ctas, STC2_THREADS, smem, st>>>(qmap, kmap, vmap, p, tab, box,
+  attn_stream_tc_kernel<D, N, kPaged><<<p.ctas, Stc2Cfg<D, N>::THREADS, smem, st>>>(qmap, kmap, vmap, p, tab, box,
                                                                           reinterpret_cast<__nv_bfloat16*>(out));
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "attn_stream_tc launch");
   prof_mark(st, "attn_stream_tc_kernel");
