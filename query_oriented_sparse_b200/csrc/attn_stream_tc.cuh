@@ -50,7 +50,7 @@ struct Stc2Cfg {
   static constexpr bool BYROW = N > 16;             // the softmax groups share rows, not tiles
   static constexpr int NR = BYROW ? N / 2 : N;      // rows per thread
   static constexpr int TMEM = N == 64 ? 256 : N == 32 ? 128 : 64;   // S twice, then O^T (one per group)
-  static constexpr int OB = BYROW ? 0 : (N * 128 + 2 * N) * 4;      // group 1's O^T, m and l of a segment
+  static constexpr int OB = BYROW ? 0 : (N * 128 + 2 * N) * 4;      // one group's O^T, m and l of a segment
   // kfull, vfull, empty per stage; qfull[2], qempty[2], sfull[2], pready[2], pfree[2]
   static constexpr int NBAR = 3 * NST + 10;
   static constexpr int FIXED = NST * STAGE + QB * Q_BYTES + 2 * P_BYTES + NBAR * 8 + 16 + NST * 4 + 16 * NR * 4 + OB + 64;
@@ -458,9 +458,11 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             finish(r, __uint_as_float(w[ri]), m[r], L);
           }
         } else {
-          // group 1 leaves its half of the segment's tiles, group 0 joins it to its own
+          // One group leaves its half of the segment's tiles, the other joins it to its own and
+          // stores: the one that the next tile (n) is not for, since its next proxy fence waits
+          // for the stores (1.2 us).
           float* ml = obuf + N * 128;
-          if (grp == 1) {
+          if (grp == (n & 1)) {
 #pragma unroll
             for (int r = 0; r < N; ++r) {
               if (r >= rows) break;
@@ -472,7 +474,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
             }
           }
           ptx::named_bar(3, 256);
-          if (grp == 0) {
+          if (grp != (n & 1)) {
 #pragma unroll
             for (int r = 0; r < N; ++r) {
               if (r >= rows || !ok) break;
@@ -488,7 +490,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
         }
       }
       ptx::tc_fence_before();
-      ptx::named_bar(3, 256);                               // the sums are read, and group 1's half
+      ptx::named_bar(3, 256);                               // the sums are read, and the half in obuf
       if (kPaged && p.own_record && ok)                     // (unit_ml and the logits are this CTA's own)
         for (int e = threadIdx.x - 64; e < sg.cnt * AST_TILE; e += 256)
           stream_record_key(p, sg, sg.span.tile(sg.i0 + e / AST_TILE) * AST_TILE + e % AST_TILE,
