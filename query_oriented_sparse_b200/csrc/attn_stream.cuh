@@ -17,7 +17,7 @@
 //
 // This file: the split, the CUDA-core kernel (fp32), the join and the record kernel.
 #pragma once
-#include "attn_decode.cuh"
+#include "attn_window.cuh"
 #include "kv_pages.cuh"
 #include "tc_ptx.cuh"
 
@@ -166,14 +166,6 @@ __device__ __forceinline__ void stream_record_key(const StreamParams& p, const S
   if (row >= 0) atomicAdd(p.record + row, w);
 }
 
-// 16-byte asynchronous copy, or 16 zero bytes when `on` is false (nothing is read then).
-__device__ __forceinline__ void ast_cp16(void* dst, const void* src, bool on) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                   (uint32_t)__cvta_generic_to_shared(dst)),
-               "l"(src), "r"(on ? 16 : 0)
-               : "memory");
-}
-
 template <typename T, int D, int R>
 constexpr int ast_smem_bytes(int batch) {
   return adc_smem_bytes<T, D, R>() + (2 * batch + 1) * 4;
@@ -237,14 +229,14 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         for (int e = lane; e < 32 * VPR; e += 32) {
           const int kk = e / VPR, vv = e - kk * VPR;
           const int rk = __shfl_sync(0xffffffffu, row, kk);
-          ast_cp16(stage + kk * ROW + vv * 16, k + (size_t)rk * D + vv * EPV, (on >> kk) & 1u);
+          adc_cp16z(stage + kk * ROW + vv * 16, k + (size_t)rk * D + vv * EPV, (on >> kk) & 1u);
         }
         adc_commit();
 #pragma unroll 4
         for (int e = lane; e < 32 * VPR; e += 32) {
           const int kk = e / VPR, vv = e - kk * VPR;
           const int rk = __shfl_sync(0xffffffffu, row, kk);
-          ast_cp16(vstage + kk * ROW + vv * 16, v + (size_t)rk * D + vv * EPV, (on >> kk) & 1u);
+          adc_cp16z(vstage + kk * ROW + vv * 16, v + (size_t)rk * D + vv * EPV, (on >> kk) & 1u);
         }
         adc_commit();
         adc_wait<1>();

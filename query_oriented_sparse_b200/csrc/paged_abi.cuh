@@ -253,16 +253,16 @@ quoka_status check_ws(const void* workspace, size_t ws_bytes, size_t need) {
 // ---- window over the contiguous cache -----------------------------------------------------
 StreamWs window_ws(const Dims& d, int max_prefix) { return stream_ws(d, (long long)max_prefix + 1, false); }
 
-template <typename T, int D>
+template <int D>
 quoka_status launch_window_simt(const Dims& d, const SeqTable& tab, long long rows, const void* q, const void* k,
                                 const void* v, int window, int n_sink, void* out, cudaStream_t st) {
-  const int s = attn_simt_smem_bytes<D>();
+  const int s = AwsCfg<D>::SMEM;
   cudaError_t e;
-  if ((e = ensure_smem(window_simt_kernel<T, D>, s)) != cudaSuccess) return cuda_fail(e, "window smem");
+  if ((e = ensure_smem(window_simt_kernel<D>, s)) != cudaSuccess) return cuda_fail(e, "window smem");
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-  window_simt_kernel<T, D><<<dim3((d.C + ATS_ROWS - 1) / ATS_ROWS, d.h_q, d.batch), ATS_THREADS, s, st>>>(
-      reinterpret_cast<const T*>(q), reinterpret_cast<const T*>(k), reinterpret_cast<const T*>(v), rows, tab, d.h_q,
-      d.h_kv, d.C, window, n_sink, reinterpret_cast<T*>(out), scale_log2);
+  window_simt_kernel<D><<<dim3((d.C + AWS_ROWS - 1) / AWS_ROWS, d.h_q, d.batch), AWS_THREADS, s, st>>>(
+      reinterpret_cast<const float*>(q), reinterpret_cast<const float*>(k), reinterpret_cast<const float*>(v), rows, tab,
+      d.h_q, d.h_kv, d.C, window, n_sink, reinterpret_cast<float*>(out), scale_log2);
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window launch");
   prof_mark(st, "window_simt_kernel");
   return QUOKA_OK;
@@ -409,8 +409,8 @@ quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, co
                                reinterpret_cast<unsigned char*>(workspace), st);
     }
     if (d.dt == QUOKA_F32)
-      return d.D == 64 ? launch_window_simt<float, 64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
-                       : launch_window_simt<float, 128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
+      return d.D == 64 ? launch_window_simt<64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
+                       : launch_window_simt<128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
     const WindowWs w = window_tc_ws(d, tab.max_prefix, window);
     if ((s = check_ws(workspace, ws_bytes, w.total)) != QUOKA_OK) return s;
     auto* ws = reinterpret_cast<unsigned char*>(workspace);
