@@ -382,8 +382,8 @@ quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, co
                                int window, int n_sink, void* out, void* workspace, size_t ws_bytes,
                                void* stream);
 
-/* Bytes of device scratch window_chunk_attn() needs (0 if the arguments are invalid; 0 for
- * fp32 chunks, and for bf16 chunks of enough query tiles to fill the GPU). */
+/* Bytes of device scratch window_chunk_attn() needs (0 if the arguments are invalid, and for
+ * chunks of enough query tiles to fill the GPU). */
 size_t window_chunk_attn_workspace_size(const quoka_shape* shape, int max_prefix, int window);
 
 /*

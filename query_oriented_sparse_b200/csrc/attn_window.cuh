@@ -1,10 +1,12 @@
 // Attention of a chunk over a sliding window of the contiguous cache and a few first
 // tokens: query t (position p = P + t) sees key j <= p when j < n_sink or j > p - window.
 //
-// CUDA-core form, for fp32 (the 1e-4 relative bound rules out tf32 products).  One CTA per
-// (sequence, query head, 64 query rows) walks the visible keys of its rows in blocks of 64:
-// the first tokens, then the window from the first row's oldest key to the last row's own,
-// with the online softmax in fp32.  It is bound by the FMA units, so a thread holds 4 x 4
+// CUDA-core form, for fp32 (the 1e-4 relative bound rules out tf32 products).  A tile is 64
+// query rows, the G query heads of a KV head at 64 / G positions each, so that short chunks
+// fill it too.  One CTA walks the visible keys of a tile in blocks of 64: the first tokens, then
+// the window from the first row's oldest key to the last row's own, with the online softmax in
+// fp32; when the tiles are few, each tile's blocks are split over several CTAs, whose partials
+// window_join_kernel merges.  It is bound by the FMA units, so a thread holds 4 x 4
 // logits and 4 x D/16 outputs and reads shared memory in 16-byte vectors along the summed
 // axis (one read for eight FMAs; rows padded by 16 bytes, so that a quarter warp's reads hit
 // all banks), and the next block's rows come in by cp.async meanwhile: SIMTFIG.  Blocks that
@@ -44,6 +46,15 @@ constexpr int AWS_ROWS = 64;
 constexpr int AWS_KEYS = 64;
 constexpr int AWS_THREADS = 256;
 
+struct WindowParams {
+  int h_q, h_kv, G, C, TP, window, n_sink;   // TP: positions per query head and tile (of one CTA)
+  int nsplit;                      // units per tile
+  long long rows_per_head;
+  float scale_log2;                // log2(e) / sqrt(d)
+  float* part;                     // [tile][unit][rows of the tile][D], then
+  float* part_ml;                  // [tile][unit][rows of the tile][2], when nsplit > 1
+};
+
 template <int D>
 struct AwsCfg {
   static constexpr int LD = D + 4;                    // padded row, floats
@@ -55,8 +66,8 @@ struct AwsCfg {
 template <int D>
 __global__ void __launch_bounds__(AWS_THREADS)
 window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cache, const float* __restrict__ v_cache,
-                   long long rows_per_head, const __grid_constant__ SeqTable tab, int h_q, int h_kv, int C,
-                   int window, int n_sink, float* __restrict__ out, float scale_log2) {
+                   const __grid_constant__ SeqTable tab, const __grid_constant__ WindowParams p,
+                   float* __restrict__ out) {
   using Cfg = AwsCfg<D>;
   constexpr int LD = Cfg::LD, LP = Cfg::LP;
   constexpr int DJ = D / 64;                          // output columns per thread: 4 at tc * 4 + 64 j
@@ -65,17 +76,24 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
   float* KVs = Qs + AWS_ROWS * LD;                    // [2][K rows padded, V rows]
   float* Ps = KVs + 2 * Cfg::KV;
 
-  const int b = blockIdx.z, h = blockIdx.y, t0 = blockIdx.x * AWS_ROWS;
-  const int G = h_q / h_kv, g = h / G;
-  const int P = tab.prefix[b];
+  const int ntp = (p.C + p.TP - 1) / p.TP;
+  const int tile = blockIdx.x / p.nsplit, part = blockIdx.x - tile * p.nsplit;
+  const int t0 = (ntp - 1 - tile % ntp) * p.TP;       // longest key ranges first
+  const int b = tile / ntp / p.h_kv, g = tile / ntp - b * p.h_kv;
+  const int P = tab.prefix[b], C = p.C, window = p.window, n_sink = p.n_sink;
   const int tid = threadIdx.x, tc = tid & 15, tr = tid >> 4;
-  const WindowSpan sp = window_span(P + t0, P + min(C, t0 + AWS_ROWS) - 1, window, n_sink);
+  const WindowSpan sp = window_span(P + t0, P + min(C, t0 + p.TP) - 1, window, n_sink);
   const int nsb = (sp.ns + AWS_KEYS - 1) / AWS_KEYS;
   const int nblk = nsb + (sp.p1 - sp.w0) / AWS_KEYS + 1;
-  const size_t head_row0 = (size_t)g * rows_per_head + tab.kv_off[b];
+  const int blk0 = (int)((long long)nblk * part / p.nsplit), blk1 = (int)((long long)nblk * (part + 1) / p.nsplit);
+  const size_t head_row0 = (size_t)g * p.rows_per_head + tab.kv_off[b];
   const float* kh = k_cache + head_row0 * D;
   const float* vh = v_cache + head_row0 * D;
-  const float* qh = q + ((size_t)(b * h_q + h) * C) * D;
+  // row r: head g G + r / TP at position t0 + r % TP; its place in q and out, -1 for none
+  auto row_at = [&](int r) {
+    const int hl = r / p.TP, t = t0 + r - hl * p.TP;
+    return hl < p.G && t < C ? (b * p.h_q + g * p.G + hl) * C + t : -1;
+  };
 
   auto start = [&](int blk) { return blk < nsb ? blk * AWS_KEYS : sp.w0 + (blk - nsb) * AWS_KEYS; };
   auto limit = [&](int blk) { return min(AWS_KEYS, (blk < nsb ? sp.ns : sp.p1 + 1) - start(blk)); };
@@ -94,9 +112,15 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
 
   for (int e = tid; e < AWS_ROWS * (D / 4); e += AWS_THREADS) {
     const int r = e / (D / 4), c = e % (D / 4) * 4;
-    adc_cp16z(Qs + r * LD + c, qh + (size_t)(t0 + r < C ? t0 + r : t0) * D + c, t0 + r < C);
+    const int at = row_at(r);
+    adc_cp16z(Qs + r * LD + c, q + (size_t)max(at, 0) * D + c, at >= 0);
   }
-  fetch(0);
+  if (blk0 < blk1) {
+    fetch(blk0);
+  } else {
+    adc_commit();
+    adc_wait<0>();
+  }
 
   float m[4], l[4], o[4][DJ][4];
 #pragma unroll
@@ -109,13 +133,16 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
       for (int e = 0; e < 4; ++e) o[i][j][e] = 0.f;
   }
 
-  for (int blk = 0; blk < nblk; ++blk) {
+  int pos[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pos[i] = P + t0 + (tr + 16 * i) % p.TP;
+  for (int blk = blk0; blk < blk1; ++blk) {
     const float* Ks = KVs + (blk & 1) * Cfg::KV;
     const float* Vs = Ks + AWS_KEYS * LD;
     const int j0 = start(blk), klim = limit(blk);
     // every row sees every key of the block (rows past C are not written)
     const bool whole = klim == AWS_KEYS && (blk < nsb || (j0 + AWS_KEYS - 1 <= P + t0 && j0 > sp.p1 - window));
-    if (blk + 1 < nblk) {
+    if (blk + 1 < blk1) {
       fetch(blk + 1);                                 // (its stage was released by the barrier below)
       adc_wait<1>();
     } else {
@@ -148,13 +175,12 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
 
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int pos = P + t0 + tr + 16 * i;
       float rmax = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int kk = j0 + tc + 16 * j;
-        const bool ok = whole || (tc + 16 * j < klim && kk <= pos && (kk < n_sink || kk > pos - window));
-        s[i][j] = ok ? s[i][j] * scale_log2 : -INFINITY;
+        const bool ok = whole || (tc + 16 * j < klim && kk <= pos[i] && (kk < n_sink || kk > pos[i] - window));
+        s[i][j] = ok ? s[i][j] * p.scale_log2 : -INFINITY;
         rmax = fmaxf(rmax, s[i][j]);
       }
 #pragma unroll
@@ -205,18 +231,67 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
     __syncthreads();                                  // the block's stage and Ps are free
   }
 
-  float* oh = out + ((size_t)(b * h_q + h) * C) * D;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int t = t0 + tr + 16 * i;
-    if (t < C) {
-      const float inv = 1.0f / l[i];                  // every row sees at least its own key
-#pragma unroll
-      for (int j = 0; j < DJ; ++j)
-        *reinterpret_cast<float4*>(oh + (size_t)t * D + tc * 4 + 64 * j) =
-            make_float4(o[i][j][0] * inv, o[i][j][1] * inv, o[i][j][2] * inv, o[i][j][3] * inv);
+    const int r = tr + 16 * i, at = row_at(r);
+    if (at < 0) continue;
+    const size_t prow = (size_t)blockIdx.x * AWS_ROWS + r;
+    const bool split = p.nsplit > 1;
+    if (split && tc == 0) {
+      p.part_ml[prow * 2] = m[i];
+      p.part_ml[prow * 2 + 1] = l[i];
     }
+    const float inv = split ? 1.f : 1.0f / l[i];      // every row sees at least its own key
+    float* dst = split ? p.part + prow * D : out + (size_t)at * D;
+#pragma unroll
+    for (int j = 0; j < DJ; ++j)
+      *reinterpret_cast<float4*>(dst + tc * 4 + 64 * j) =
+          make_float4(o[i][j][0] * inv, o[i][j][1] * inv, o[i][j][2] * inv, o[i][j][3] * inv);
   }
+}
+
+// Joins the units of each tile: out = sum_u O_u 2^(m_u - M) / sum_u l_u 2^(m_u - M).  One thread
+// per 8 output columns.  CTAS CTAs of ROWS rows to a tile.
+constexpr int AWJ_THREADS = 256;
+template <typename T, int D, int CTAS, int ROWS>
+__global__ void __launch_bounds__(AWJ_THREADS)
+window_join_kernel(const __grid_constant__ WindowParams p, long long total, T* __restrict__ out) {
+  constexpr int VPR = D / 8;
+  const long long e = (long long)blockIdx.x * AWJ_THREADS + threadIdx.x;
+  if (e >= total) return;
+  const long long row = e / VPR;           // (b * h_q + h) * C + t
+  const int c = (int)(e - row * VPR) * 8;
+  const int t = (int)(row % p.C);
+  const long long bh = row / p.C;
+  const int b = (int)(bh / p.h_q), h = (int)(bh - (long long)b * p.h_q);
+  const int g = h / p.G, hl = h - g * p.G;
+  const int span = CTAS * p.TP, ntp = (p.C + span - 1) / span;
+  const int in = t % span, rank = in / p.TP;
+  const long long tile = ((long long)b * p.h_kv + g) * ntp + (ntp - 1 - t / span);
+  const size_t r0 = ((size_t)tile * p.nsplit * CTAS + rank) * ROWS + hl * p.TP + in % p.TP;
+  const size_t step = (size_t)CTAS * ROWS;
+  float M = -INFINITY, L = 0.f, o[8];
+  for (int s = 0; s < p.nsplit; ++s)
+    if (p.part_ml[(r0 + s * step) * 2 + 1] != 0.f) M = fmaxf(M, p.part_ml[(r0 + s * step) * 2]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) o[i] = 0.f;
+  for (int s = 0; s < p.nsplit; ++s) {
+    const float l = p.part_ml[(r0 + s * step) * 2 + 1];
+    if (l == 0.f) continue;                // no visible key: its O is not set
+    const float f = exp2f(p.part_ml[(r0 + s * step) * 2] - M);
+    L = fmaf(l, f, L);
+    const float4* src = reinterpret_cast<const float4*>(p.part + (r0 + s * step) * D + c);
+    const float4 a = src[0], d = src[1];
+    o[0] = fmaf(a.x, f, o[0]); o[1] = fmaf(a.y, f, o[1]); o[2] = fmaf(a.z, f, o[2]); o[3] = fmaf(a.w, f, o[3]);
+    o[4] = fmaf(d.x, f, o[4]); o[5] = fmaf(d.y, f, o[5]); o[6] = fmaf(d.z, f, o[6]); o[7] = fmaf(d.w, f, o[7]);
+  }
+  const float inv = 1.f / L;
+  __align__(16) T y[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) y[i] = from_f32<T>(o[i] * inv);
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(y) / 16; ++i)
+    reinterpret_cast<uint4*>(out + e * 8)[i] = *reinterpret_cast<const uint4*>(reinterpret_cast<const unsigned char*>(y) + 16 * i);
 }
 
 }  // namespace quoka

@@ -63,15 +63,6 @@ struct AwtCfg {
   static constexpr int SMEM = 1024 + 2 * STREAM + (2 * BARS + 1) * 8 + 8 + 16 + 16 + XBUF + MBUF;
 };
 
-struct WindowTcParams {
-  int h_q, h_kv, G, C, TP, window, n_sink;
-  int nsplit;                      // units per tile
-  long long rows_per_head;
-  float scale_log2;                // log2(e) / sqrt(d)
-  float* part;                     // [tile][unit][rows of the cluster][D], then
-  float* part_ml;                  // [tile][unit][rows of the cluster][2], when nsplit > 1
-};
-
 // A unit of work: blocks [j0, j1) of the nblk blocks of a tile.
 struct WindowUnit {
   int b, g, t0;
@@ -89,7 +80,7 @@ struct WindowUnit {
   }
 };
 
-__device__ __forceinline__ WindowUnit window_unit(const WindowTcParams& p, const SeqTable& tab, int unit, int ntp,
+__device__ __forceinline__ WindowUnit window_unit(const WindowParams& p, const SeqTable& tab, int unit, int ntp,
                                                   int span) {
   WindowUnit u;
   const unsigned tile = (unsigned)unit / (unsigned)p.nsplit, rest = tile / (unsigned)ntp;
@@ -175,7 +166,7 @@ template <int D>
 __global__ void __cluster_dims__(D == 128 ? 2 : 1, 1, 1) __launch_bounds__(AWT_THREADS, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ SeqTable tab,
-                 const __grid_constant__ WindowTcParams p, const __nv_bfloat16* __restrict__ v_cache,
+                 const __grid_constant__ WindowParams p, const __nv_bfloat16* __restrict__ v_cache,
                  __nv_bfloat16* __restrict__ out) {
   using Cfg = AwtCfg<D>;
   constexpr bool PAIR = Cfg::PAIR;
@@ -698,51 +689,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     if constexpr (PAIR) ptx::tmem_dealloc_pair(tmem, 512);
     else ptx::tmem_dealloc(tmem, 512);
   }
-}
-
-// Joins the units of each tile: out = sum_u O_u 2^(m_u - M) / sum_u l_u 2^(m_u - M).  One thread
-// per 8 output columns.
-constexpr int AWJ_THREADS = 256;
-template <int D>
-__global__ void __launch_bounds__(AWJ_THREADS)
-window_join_kernel(const __grid_constant__ WindowTcParams p, long long total, __nv_bfloat16* __restrict__ out) {
-  using Cfg = AwtCfg<D>;
-  constexpr int VPR = D / 8;
-  const long long e = (long long)blockIdx.x * AWJ_THREADS + threadIdx.x;
-  if (e >= total) return;
-  const long long row = e / VPR;           // (b * h_q + h) * C + t
-  const int c = (int)(e - row * VPR) * 8;
-  const int t = (int)(row % p.C);
-  const long long bh = row / p.C;
-  const int b = (int)(bh / p.h_q), h = (int)(bh - (long long)b * p.h_q);
-  const int g = h / p.G, hl = h - g * p.G;
-  const int span = Cfg::CTAS * p.TP, ntp = (p.C + span - 1) / span;
-  const int in = t % span, rank = in / p.TP;
-  const long long tile = ((long long)b * p.h_kv + g) * ntp + (ntp - 1 - t / span);
-  const size_t r0 = ((size_t)tile * p.nsplit * Cfg::CTAS + rank) * 128 + hl * p.TP + in % p.TP;
-  const size_t step = (size_t)Cfg::CTAS * 128;
-  float M = -INFINITY, L = 0.f, o[8];
-  for (int s = 0; s < p.nsplit; ++s)
-    if (p.part_ml[(r0 + s * step) * 2 + 1] != 0.f) M = fmaxf(M, p.part_ml[(r0 + s * step) * 2]);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = 0.f;
-  for (int s = 0; s < p.nsplit; ++s) {
-    const float l = p.part_ml[(r0 + s * step) * 2 + 1];
-    if (l == 0.f) continue;                // no visible key: its O is not set
-    const float f = exp2f(p.part_ml[(r0 + s * step) * 2] - M);
-    L = fmaf(l, f, L);
-    const float4* src = reinterpret_cast<const float4*>(p.part + (r0 + s * step) * D + c);
-    const float4 a = src[0], d = src[1];
-    o[0] = fmaf(a.x, f, o[0]); o[1] = fmaf(a.y, f, o[1]); o[2] = fmaf(a.z, f, o[2]); o[3] = fmaf(a.w, f, o[3]);
-    o[4] = fmaf(d.x, f, o[4]); o[5] = fmaf(d.y, f, o[5]); o[6] = fmaf(d.z, f, o[6]); o[7] = fmaf(d.w, f, o[7]);
-  }
-  const float inv = 1.f / L;
-  uint4 w;
-  w.x = pack_bf16x2(o[0] * inv, o[1] * inv);
-  w.y = pack_bf16x2(o[2] * inv, o[3] * inv);
-  w.z = pack_bf16x2(o[4] * inv, o[5] * inv);
-  w.w = pack_bf16x2(o[6] * inv, o[7] * inv);
-  reinterpret_cast<uint4*>(out)[e] = w;
 }
 
 }  // namespace quoka

@@ -253,46 +253,78 @@ quoka_status check_ws(const void* workspace, size_t ws_bytes, size_t need) {
 // ---- window over the contiguous cache -----------------------------------------------------
 StreamWs window_ws(const Dims& d, int max_prefix) { return stream_ws(d, (long long)max_prefix + 1, false); }
 
-template <int D>
-quoka_status launch_window_simt(const Dims& d, const SeqTable& tab, long long rows, const void* q, const void* k,
-                                const void* v, int window, int n_sink, void* out, cudaStream_t st) {
-  const int s = AwsCfg<D>::SMEM;
-  cudaError_t e;
-  if ((e = ensure_smem(window_simt_kernel<D>, s)) != cudaSuccess) return cuda_fail(e, "window smem");
-  const float scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-  window_simt_kernel<D><<<dim3((d.C + AWS_ROWS - 1) / AWS_ROWS, d.h_q, d.batch), AWS_THREADS, s, st>>>(
-      reinterpret_cast<const float*>(q), reinterpret_cast<const float*>(k), reinterpret_cast<const float*>(v), rows, tab,
-      d.h_q, d.h_kv, d.C, window, n_sink, reinterpret_cast<float*>(out), scale_log2);
-  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window launch");
-  prof_mark(st, "window_simt_kernel");
-  return QUOKA_OK;
-}
-
-// Units per tile of the tensor-core form and the space of their partials.
-constexpr int WINDOW_PAIRS = 74;              // clusters of two SMs, whose two streams share a unit
-constexpr int WINDOW_SINGLES = 148;
-constexpr int WINDOW_MIN_BLOCKS = 8;          // 128-key blocks per unit at least
+// Tiles of the chunk forms, units per tile and the space of their partials.  A tile holds
+// (rows / G) positions: bf16 d 128 two CTAs of 128 rows, bf16 d 64 one, fp32 one of 64 rows.
+constexpr int WINDOW_PAIRS = 74;              // bf16, d 128: clusters of two SMs, whose two streams share a unit
+constexpr int WINDOW_SINGLES = 148;           // bf16, d 64; fp32
+constexpr int WINDOW_MIN_BLOCKS = 8;          // 128-key (fp32: 64-key) blocks per unit at least
 constexpr int WINDOW_MAX_SPLIT = 32;
 
 struct WindowWs {
   long long tiles;
-  int nsplit;
+  int TP, nsplit;
   size_t part, part_ml, total;
 };
 
-WindowWs window_tc_ws(const Dims& d, int max_prefix, int window) {
+WindowWs window_tile_ws(const Dims& d, int max_prefix, int window) {
   WindowWs w;
-  const bool pair = d.D == 128;
-  const int ctas = pair ? 2 : 1, span = ctas * (128 / d.G);
+  const bool tc = d.dt == QUOKA_BF16, pair = tc && d.D == 128;
+  const int ctas = pair ? 2 : 1, cta_rows = tc ? 128 : AWS_ROWS, keys = tc ? AWT_BK : AWS_KEYS;
+  w.TP = cta_rows / d.G;
+  const int span = ctas * w.TP;
   w.tiles = (long long)((d.C + span - 1) / span) * d.h_kv * d.batch;
-  const long long blocks = (std::min<long long>(window, (long long)max_prefix + 1) + span + AWT_BK - 1) / AWT_BK;
+  const long long blocks = (std::min<long long>(window, (long long)max_prefix + 1) + span + keys - 1) / keys;
   const long long room = (pair ? WINDOW_PAIRS : WINDOW_SINGLES) / w.tiles;
   w.nsplit = (int)std::max<long long>(1, std::min(std::min(room, blocks / WINDOW_MIN_BLOCKS), (long long)WINDOW_MAX_SPLIT));
-  const size_t rows = w.nsplit > 1 ? (size_t)w.tiles * w.nsplit * ctas * 128 : 0;
+  const size_t rows = w.nsplit > 1 ? (size_t)w.tiles * w.nsplit * ctas * cta_rows : 0;
   w.part = 0;
   w.part_ml = align_up(rows * d.D * 4, 256);
   w.total = align_up(w.part_ml + rows * 8, 256);
   return w;
+}
+
+WindowParams window_params(const Dims& d, long long rows, int window, int n_sink, unsigned char* ws, const WindowWs& w) {
+  WindowParams p;
+  p.h_q = d.h_q;
+  p.h_kv = d.h_kv;
+  p.G = d.G;
+  p.C = d.C;
+  p.TP = w.TP;
+  p.window = window;
+  p.n_sink = n_sink;
+  p.nsplit = w.nsplit;
+  p.rows_per_head = rows;
+  p.scale_log2 = 1.4426950408889634f / sqrtf((float)d.D);
+  p.part = reinterpret_cast<float*>(ws + w.part);
+  p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+  return p;
+}
+
+template <typename T, int D, int CTAS, int ROWS>
+quoka_status launch_window_join(const Dims& d, const WindowParams& p, void* out, cudaStream_t st) {
+  if (p.nsplit == 1) return QUOKA_OK;
+  const long long total = (long long)d.batch * d.h_q * d.C * (D / 8);
+  window_join_kernel<T, D, CTAS, ROWS><<<(unsigned)((total + AWJ_THREADS - 1) / AWJ_THREADS), AWJ_THREADS, 0, st>>>(
+      p, total, reinterpret_cast<T*>(out));
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "window_join launch");
+  prof_mark(st, "window_join_kernel");
+  return QUOKA_OK;
+}
+
+template <int D>
+quoka_status launch_window_simt(const Dims& d, const SeqTable& tab, long long rows, const void* q, const void* k,
+                                const void* v, int window, int n_sink, void* out, unsigned char* ws, const WindowWs& w,
+                                cudaStream_t st) {
+  const WindowParams p = window_params(d, rows, window, n_sink, ws, w);
+  cudaError_t e;
+  if ((e = ensure_smem(window_simt_kernel<D>, AwsCfg<D>::SMEM)) != cudaSuccess) return cuda_fail(e, "window smem");
+  window_simt_kernel<D><<<(unsigned)(w.tiles * w.nsplit), AWS_THREADS, AwsCfg<D>::SMEM, st>>>(
+      reinterpret_cast<const float*>(q), reinterpret_cast<const float*>(k), reinterpret_cast<const float*>(v), tab, p,
+      reinterpret_cast<float*>(out));
+  if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window launch");
+  prof_mark(st, "window_simt_kernel");
+  return launch_window_join<float, D, 1, AWS_ROWS>(d, p, out, st);
 }
 
 // Clusters of the window kernel that fit on the device at once.
@@ -324,20 +356,7 @@ quoka_status launch_window_tc(const Dims& d, const SeqTable& tab, long long rows
                               const void* v, int window, int n_sink, void* out, unsigned char* ws, const WindowWs& w,
                               cudaStream_t st) {
   using Cfg = AwtCfg<D>;
-  WindowTcParams p;
-  p.h_q = d.h_q;
-  p.h_kv = d.h_kv;
-  p.G = d.G;
-  p.C = d.C;
-  p.TP = 128 / d.G;
-  p.window = window;
-  p.n_sink = n_sink;
-  p.nsplit = w.nsplit;
-  p.rows_per_head = rows;
-  p.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
-  p.part = reinterpret_cast<float*>(ws + w.part);
-  p.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
-  if (w.tiles * w.nsplit >= (1ll << 30)) return fail(QUOKA_ERR_UNSUPPORTED, "more than 2^30 query tiles");
+  const WindowParams p = window_params(d, rows, window, n_sink, ws, w);
   CUtensorMap qmap, kmap, vmap;
   quoka_status s;
   const uint64_t kv_rows = (uint64_t)d.h_kv * rows;
@@ -353,14 +372,7 @@ quoka_status launch_window_tc(const Dims& d, const SeqTable& tab, long long rows
                                                                   reinterpret_cast<__nv_bfloat16*>(out));
   if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_tc launch");
   prof_mark(st, "window_tc_kernel");
-  if (w.nsplit > 1) {
-    const long long total = (long long)d.batch * d.h_q * d.C * (D / 8);
-    window_join_kernel<D><<<(unsigned)((total + AWJ_THREADS - 1) / AWJ_THREADS), AWJ_THREADS, 0, st>>>(
-        p, total, reinterpret_cast<__nv_bfloat16*>(out));
-    if ((e = cudaGetLastError()) != cudaSuccess) return cuda_fail(e, "window_join launch");
-    prof_mark(st, "window_join_kernel");
-  }
-  return QUOKA_OK;
+  return launch_window_join<__nv_bfloat16, D, Cfg::CTAS, 128>(d, p, out, st);
 }
 
 }  // namespace
@@ -371,7 +383,7 @@ size_t window_chunk_attn_workspace_size(const quoka_shape* shape, int max_prefix
   Dims d;
   if (check_shape(shape, &d) != QUOKA_OK || max_prefix < 0 || window < 1) return 0;
   if (d.C == 1) return window_ws(d, max_prefix).total;
-  return d.dt == QUOKA_BF16 ? window_tc_ws(d, max_prefix, window).total : 0;
+  return window_tile_ws(d, max_prefix, window).total;
 }
 
 quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, const void* k_cache,
@@ -408,12 +420,13 @@ quoka_status window_chunk_attn(const quoka_shape* shape, const void* q_chunk, co
       return run_stream<false>(d, tab, p, w, q_chunk, k_cache, v_cache, out,
                                reinterpret_cast<unsigned char*>(workspace), st);
     }
-    if (d.dt == QUOKA_F32)
-      return d.D == 64 ? launch_window_simt<64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st)
-                       : launch_window_simt<128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, st);
-    const WindowWs w = window_tc_ws(d, tab.max_prefix, window);
+    const WindowWs w = window_tile_ws(d, tab.max_prefix, window);
+    if (w.tiles * w.nsplit >= (1ll << 30)) return fail(QUOKA_ERR_UNSUPPORTED, "more than 2^30 query tiles");
     if ((s = check_ws(workspace, ws_bytes, w.total)) != QUOKA_OK) return s;
     auto* ws = reinterpret_cast<unsigned char*>(workspace);
+    if (d.dt == QUOKA_F32)
+      return d.D == 64 ? launch_window_simt<64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, ws, w, st)
+                       : launch_window_simt<128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, ws, w, st);
     return d.D == 64 ? launch_window_tc<64>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, ws, w, st)
                      : launch_window_tc<128>(d, tab, rows, q_chunk, k_cache, v_cache, window, n_sink, out, ws, w, st);
   });

@@ -192,12 +192,13 @@ def test_graph_replay_and_other_stream(cuda_device):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
 @pytest.mark.parametrize("d", [64, 128])
-def test_bad_rows_in_split_tiles(d, cuda_device):
+def test_bad_rows_in_split_tiles(d, dtype, cuda_device):
     """As above with each tile's keys split over several units."""
     prefix, window, n_sink, C = (2500,), 2000, 0, 12
-    q, k, v, off = make(8, 2, d, C, prefix, BF, seed=6)
-    assert Bd.window_workspace_size(Bd.make_shape(1, 8, 2, d, C, BF), 2500, window) > 0
+    q, k, v, off = make(8, 2, d, C, prefix, dtype, seed=6)
+    assert Bd.window_workspace_size(Bd.make_shape(1, 8, 2, d, C, dtype), 2500, window) > 0
     clean = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), off, prefix, window, n_sink).cpu()
     for at in (2500 + 7, 2500 - 1995, 2500 + 11):
         v2 = v.clone()
@@ -250,13 +251,13 @@ def test_rejects(case, status):
 
 
 def test_workspace_size():
-    for C, dtype, window in ((1, BF, 100), (1, F32, 100), (16, BF, 4096)):
+    for C, dtype, window in ((1, BF, 100), (1, F32, 100), (16, BF, 4096), (16, F32, 4096)):
         n = Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, C, dtype), 4096, window)
         assert n > 0 and n % 256 == 0
-    # one unit per tile: short windows, many tiles, fp32
+    # one unit per tile: short windows, many tiles
     assert Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, 64, BF), 4096, 100) == 0
     assert Bd.window_workspace_size(Bd.make_shape(8, 32, 8, 128, 4096, BF), 4096, 4096) == 0
-    assert Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, 16, F32), 4096, 4096) == 0
+    assert Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 128, 4096, F32), 4096, 100) == 0
     assert Bd.window_workspace_size(Bd.make_shape(2, 8, 2, 96, 16, BF), 4096, 4096) == 0
 
 
