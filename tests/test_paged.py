@@ -328,7 +328,8 @@ def test_evict_ties_and_odd_records(cuda_device):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("h_kv,B,n", [(1, 1, 60000), (8, 1, 9000), (8, 4, 3000), (2, 80, 500), (1, 1, 200000)])
+@pytest.mark.parametrize("h_kv,B,n", [(1, 1, 60000), (8, 1, 9000), (8, 2, 9000), (8, 4, 3000), (8, 8, 3000),
+                                      (2, 80, 500), (1, 1, 200000), (4, 32, 30000)])
 def test_evict_launch_forms(h_kv, B, n, cuda_device):
     """Rows over clusters of 16 CTAs down to one."""
     page, budget = 64, n // 7
@@ -409,6 +410,133 @@ def test_prompt_from_the_contiguous_cache_into_pages(cuda_device):
         a = cache.attend(qt, window=window, n_sink=n_sink)
         b = Bd.window_chunk_attn(qt, k, v, (0, n), (n - 1,), window, n_sink)
         assert torch.equal(a, b)
+
+
+# ---- calls that a serving loop makes in other ways ------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_decode_largest_batch(dtype, cuda_device):
+    lens = [(53 * i) % 97 for i in range(1023)] + [700]
+    pool = Pool(1, 64, 8, lens, dtype, seed=30)
+    q = torch.randn(1024, 4, 1, 64, generator=torch.Generator().manual_seed(31)).to(dtype)
+    out, w = run_decode(pool, q, record=True)
+    assert Bd.device_error() == 0
+    check_decode(pool, q, None, 0, out, w)
+
+
+@pytest.mark.gpu
+def test_two_calls_at_once_on_two_streams(cuda_device):
+    pools = [Pool(2, 128, 16, (3000, 77), BF, seed=32), Pool(2, 128, 16, (1200, 2500), BF, seed=33)]
+    qs = [torch.randn(2, 8, 1, 128, generator=torch.Generator().manual_seed(34 + i)).to(BF) for i in range(2)]
+    want = [run_decode(p, q)[0] for p, q in zip(pools, qs)]
+    args = [(q.cuda(), *p.gpu()) for p, q in zip(pools, qs)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [Bd.paged_decode_attn(q, k, v, t, n, max(p.lens), stream=s)
+                for (q, k, v, t, n), p, s in zip(args, pools, streams)]
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o.cpu(), w)
+
+
+@pytest.mark.gpu
+def test_a_step_with_eviction_in_a_graph(cuda_device):
+    """append, attention with the record and eviction captured once and replayed as the
+    lengths change."""
+    page, B, h_kv, d = 16, 2, 2, 128
+    lens = (400, 399)
+    pool = Pool(h_kv, d, page, [n + 40 for n in lens], BF, seed=36, spare=40)
+    k, v, table, _ = pool.gpu()
+    w = pool.w.nan_to_num(0.5).cuda()
+    start = torch.tensor(lens, dtype=torch.int32).cuda()
+    budget = torch.tensor([64, 64], dtype=torch.int32).cuda()
+    dst = torch.tensor(pool.free[:8], dtype=torch.int32).view(2, 4).cuda()
+    g = torch.Generator().manual_seed(37)
+    kn, vn, q = (torch.randn(B, h, 1, d, generator=g).to(BF).cuda() for h in (h_kv, h_kv, 8))
+    idx = torch.zeros(B, h_kv, 64, dtype=torch.int32, device="cuda")
+    new = torch.zeros(B, dtype=torch.int32, device="cuda")
+    out = torch.empty_like(q)
+    n1 = torch.empty_like(start)
+
+    def step():
+        Bd.paged_append(kn, vn, k, v, table, start, weight_pages=w)
+        torch.add(start, 1, out=n1)
+        Bd.paged_decode_attn(q, k, v, table, n1, 440, weight_pages=w, out=out)
+        Bd.paged_evict(k, v, w, table, n1, 440, budget, 64, dst, n_sink=2, n_recent=8, idx_out=idx, new_len=new)
+
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for now in (lens, (30, 439), (0, 63)):
+        start.copy_(torch.tensor(now, dtype=torch.int32))
+        w.copy_(torch.rand(w.shape, generator=g))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert Bd.device_error() == 0
+        assert new.cpu().tolist() == [min(n + 1, 64) for n in now]
+        for b, n in enumerate(now):
+            rec = R.gather_pages(w.cpu(), table[b].cpu(), n + 1)
+            ks, vs = (R.gather_pages(t.cpu(), table[b].cpu(), n + 1) for t in (k, v))
+            assert torch.equal(ks[:, n], kn[b, :, 0].cpu()) and torch.equal(vs[:, n], vn[b, :, 0].cpu())
+            m = min(n + 1, 64)
+            for h in range(h_kv):
+                rows = R.evict_rows(rec[h], n + 1, 64, 2, 8)
+                assert idx[b, h, :m].tolist() == rows
+                assert torch.equal(R.gather_pages(k.cpu(), dst[b].cpu(), m)[h], ks[h][rows])
+            for h in range(8):
+                o, mag, _, S = R.attend(q[b, h].cpu().double(), ks[h // 4].double(), vs[h // 4].double(),
+                                        torch.ones(1, n + 1, dtype=torch.bool))
+                R.assert_close(out[b, h].cpu(), o, R.out_tol(o, mag, S, d, n + 1, BF), f"length {n} head {h}")
+
+
+@pytest.mark.gpu
+def test_pools_past_32_bit_offsets(cuda_device):
+    """Pools of more than 2^31 elements each, the sequence in their last pages."""
+    page, h_kv, d, N = 64, 4, 128, 66000
+    k, v = (torch.empty(N, h_kv, page, d, dtype=BF, device="cuda") for _ in range(2))
+    w = torch.zeros(N, h_kv, page, device="cuda")
+    assert k.numel() > 2 ** 31
+    n = 300
+    table = torch.tensor([[N - 1, N - 3, N - 2, N - 5, N - 4]], dtype=torch.int32)
+    g = torch.Generator().manual_seed(38)
+    kn, vn = (torch.randn(1, h_kv, n, d, generator=g).to(BF) for _ in range(2))
+    zero = torch.zeros(1, dtype=torch.int32).cuda()
+    Bd.paged_append(kn.cuda(), vn.cuda(), k, v, table.cuda(), zero, weight_pages=w)
+    q = torch.randn(1, 16, 1, d, generator=g).to(BF)
+    ln = torch.tensor([n], dtype=torch.int32).cuda()
+    out = Bd.paged_decode_attn(q.cuda(), k, v, table.cuda(), ln, n, weight_pages=w).cpu()
+    for h in range(16):
+        o, mag, _, S = R.attend(q[0, h].double(), kn[0, h // 4].double(), vn[0, h // 4].double(),
+                                torch.ones(1, n, dtype=torch.bool))
+        R.assert_close(out[0, h], o, R.out_tol(o, mag, S, d, n, BF), f"head {h}")
+    dst = torch.tensor([[N - 7, N - 6]], dtype=torch.int32)
+    idx, _ = Bd.paged_evict(k, v, w, table.cuda(), ln, n, torch.tensor([100], dtype=torch.int32).cuda(), 100, dst.cuda())
+    rec = w[table[0].long().cuda()].transpose(0, 1).reshape(h_kv, -1)[:, :n].cpu()
+    moved = k[dst[0].long().cuda()].transpose(0, 1).reshape(h_kv, -1, d)[:, :100].cpu()
+    for h in range(h_kv):
+        rows = R.evict_rows(rec[h], n, 100, 0, 0)
+        assert idx[0, h].tolist() == rows
+        assert torch.equal(moved[h], kn[0, h][rows])
+    assert Bd.device_error() == 0
+
+
+@pytest.mark.gpu
+def test_counts_and_budgets_out_of_range_are_reported(cuda_device):
+    pool = Pool(2, 64, 8, (24, 24), F32, seed=39, spare=10)
+    k, v, table, lens = pool.gpu()
+    kn = torch.randn(2, 2, 4, 64).cuda()
+    Bd.paged_append(kn, kn, k, v, table, torch.tensor([0, 0], dtype=torch.int32).cuda(),
+                    n_new=torch.tensor([9, -2], dtype=torch.int32).cuda())
+    assert Bd.device_error() == 4
+    assert torch.equal(R.gather_pages(k.cpu(), table[0].cpu(), 4), kn[0].cpu())
+    assert torch.equal(R.gather_pages(k.cpu(), table[1].cpu(), 24), R.gather_pages(pool.k, pool.table[1], 24))
+    dst = torch.tensor(pool.free[:2], dtype=torch.int32).view(2, 1).cuda()
+    _, new = Bd.paged_evict(k, v, pool.w.cuda(), table, lens, 24, torch.tensor([50, -1], dtype=torch.int32).cuda(), 8, dst)
+    assert Bd.device_error() == 4
+    assert new.cpu().tolist() == [8, 0]
 
 
 # ---- refusals (host checks) --------------------------------------------------------------------

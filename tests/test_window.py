@@ -211,6 +211,30 @@ def test_bad_rows_in_split_tiles(d, dtype, cuda_device):
         assert out[0][:, sees, 11].isnan().all() and torch.isfinite(out[0][:, sees, :11].float()).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [1, 40])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_long_prefix(dtype, C, cuda_device):
+    prefix, window, n_sink = (120001,), 3001, 70
+    q, k, v, off = make(4, 1, 64, C, prefix, dtype, seed=7)
+    out = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), off, prefix, window, n_sink)
+    check(q, k, v, off, prefix, window, n_sink, out.cpu())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [1, 33])
+def test_cache_past_32_bit_offsets(C, cuda_device):
+    """A cache of more than 2^31 elements, the sequence in its last rows."""
+    rows, P, d = 16800000, 500, 128
+    q, k, v, _ = make(8, 1, d, C, (P,), BF, seed=8)
+    kb, vb = (torch.empty(1, rows, d, dtype=BF, device="cuda") for _ in range(2))
+    assert kb.numel() > 2 ** 31
+    off = [0, rows - P - C, rows]
+    kb[:, off[1]:], vb[:, off[1]:] = k.cuda(), v.cuda()
+    whole = Bd.window_chunk_attn(q.cuda(), kb, vb, (off[1], rows), (P,), 200, 3)
+    check(q, k, v, [0, P + C], (P,), 200, 3, whole.cpu())
+
+
 # ---- refusals (host checks: no GPU needed, nothing is launched) --------------------------------
 
 no_gpu = pytest.mark.skipif(torch.cuda.is_available(),
