@@ -173,6 +173,7 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
         }
     }
 
+    float al[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float rmax = -INFINITY;
@@ -187,7 +188,7 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
       for (int off = 8; off > 0; off >>= 1) rmax = fmaxf(rmax, __shfl_xor_sync(0xffffffffu, rmax, off));
       const float mnew = fmaxf(m[i], rmax);
       const float muse = (mnew == -INFINITY) ? 0.f : mnew;
-      const float alpha = exp2f(m[i] - muse);
+      al[i] = exp2f(m[i] - muse);
       float rsum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -197,14 +198,19 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
       }
 #pragma unroll
       for (int off = 8; off > 0; off >>= 1) rsum += __shfl_xor_sync(0xffffffffu, rsum, off);
-      l[i] = l[i] * alpha + rsum;
+      l[i] = l[i] * al[i] + rsum;
       m[i] = mnew;
+    }
+    __syncwarp();                                     // a row's weights are written and read by one warp
+    // the block's P.V is summed by itself, so that no sum runs over more than 64 keys or over
+    // the blocks
+    float ob[4][DJ][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < DJ; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[i][j][e] *= alpha;
-    }
-    __syncwarp();                                     // a row's weights are written and read by one warp
+        for (int e = 0; e < 4; ++e) ob[i][j][e] = 0.f;
     for (int kk = 0; kk < klim; kk += 4) {
       float4 pv[4];
 #pragma unroll
@@ -220,14 +226,20 @@ window_simt_kernel(const float* __restrict__ q, const float* __restrict__ k_cach
           if (!whole && pr == 0.f) continue;
 #pragma unroll
           for (int j = 0; j < DJ; ++j) {
-            o[i][j][0] = fmaf(pr, vv[j].x, o[i][j][0]);
-            o[i][j][1] = fmaf(pr, vv[j].y, o[i][j][1]);
-            o[i][j][2] = fmaf(pr, vv[j].z, o[i][j][2]);
-            o[i][j][3] = fmaf(pr, vv[j].w, o[i][j][3]);
+            ob[i][j][0] = fmaf(pr, vv[j].x, ob[i][j][0]);
+            ob[i][j][1] = fmaf(pr, vv[j].y, ob[i][j][1]);
+            ob[i][j][2] = fmaf(pr, vv[j].z, ob[i][j][2]);
+            ob[i][j][3] = fmaf(pr, vv[j].w, ob[i][j][3]);
           }
         }
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < DJ; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][j][e] = fmaf(o[i][j][e], al[i], ob[i][j][e]);
     __syncthreads();                                  // the block's stage and Ps are free
   }
 
