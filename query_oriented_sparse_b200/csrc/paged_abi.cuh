@@ -110,9 +110,11 @@ cudaError_t launch_dependent(void (*kern)(P...), dim3 grid, unsigned block, size
 }
 
 template <typename T, int D, int R, bool kPaged>
-cudaError_t launch_stream_simt(const StreamParams& p, const SeqTable& tab, const void* q, const void* k,
+cudaError_t launch_stream_simt(StreamParams& p, const SeqTable& tab, int max_ctas, const void* q, const void* k,
                                const void* v, void* out, cudaStream_t st) {
   const int smem = ast_smem_bytes<T, D, R>(p.batch);
+  // as many CTAs as fit the SMs at once
+  if (!p.by_unit) p.ctas = std::min(max_ctas, sm_count() * std::max(1, std::min(4, 230000 / (smem + 1024))));
   cudaError_t e = ensure_smem(attn_stream_kernel<T, D, R, kPaged>, smem);
   if (e != cudaSuccess) return e;
   attn_stream_kernel<T, D, R, kPaged><<<dim3(p.ctas, (p.G + R - 1) / R), AdcCfg<T, D>::THREADS, smem, st>>>(
@@ -121,20 +123,18 @@ cudaError_t launch_stream_simt(const StreamParams& p, const SeqTable& tab, const
   return cudaGetLastError();
 }
 
-// fp32: query heads of a group in rows of up to 16 per CTA, as many CTAs as fit the SMs at once.
+// fp32: query heads of a group in rows of up to 16 per CTA.
 template <typename T, int D, bool kPaged>
 cudaError_t launch_stream_rows(StreamParams& p, const SeqTable& tab, int max_ctas, const void* q, const void* k,
                                const void* v, void* out, cudaStream_t st) {
   int r = 1;
   while (r < std::min(p.G, 16)) r *= 2;
-  const int per_sm = std::max(1, std::min(4, 230000 / (ast_smem_bytes<T, D, 16>(p.batch) + 1024)));
-  if (!p.by_unit) p.ctas = std::min(max_ctas, sm_count() * per_sm);
   switch (r) {
-    case 1: return launch_stream_simt<T, D, 1, kPaged>(p, tab, q, k, v, out, st);
-    case 2: return launch_stream_simt<T, D, 2, kPaged>(p, tab, q, k, v, out, st);
-    case 4: return launch_stream_simt<T, D, 4, kPaged>(p, tab, q, k, v, out, st);
-    case 8: return launch_stream_simt<T, D, 8, kPaged>(p, tab, q, k, v, out, st);
-    default: return launch_stream_simt<T, D, 16, kPaged>(p, tab, q, k, v, out, st);
+    case 1: return launch_stream_simt<T, D, 1, kPaged>(p, tab, max_ctas, q, k, v, out, st);
+    case 2: return launch_stream_simt<T, D, 2, kPaged>(p, tab, max_ctas, q, k, v, out, st);
+    case 4: return launch_stream_simt<T, D, 4, kPaged>(p, tab, max_ctas, q, k, v, out, st);
+    case 8: return launch_stream_simt<T, D, 8, kPaged>(p, tab, max_ctas, q, k, v, out, st);
+    default: return launch_stream_simt<T, D, 16, kPaged>(p, tab, max_ctas, q, k, v, out, st);
   }
 }
 
