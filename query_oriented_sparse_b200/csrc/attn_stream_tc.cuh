@@ -13,13 +13,17 @@
 // sum and O^T, joined at the end of a segment; for more rows, where a tile's exponentials
 // weigh more than its barriers, each takes half of the rows of every tile.
 //
-// Warps 0 and 11 load: pages are copied box by box (a box is the largest power of two of rows that
-// divides the page size, at most 128), only boxes with a visible key, and marks the boxes
-// whose page was bad.  A paged box is one copy: the tensor map splits rows into groups of
-// eight and their two 128-byte halves, so that the copy lays down whole swizzle atoms
-// [group][half][8 rows] (two copies per 16-row page and operand, instead of four, took the
-// 32-sequence decode step with pages of 16 from PAGEFIG).  Warp 1 issues S, warp 10 P.V, warps
-// 2-9 run the softmax, one thread per key: its logits come with one TMEM load.  The running
+// Loads: pages are copied box by box (a box is the largest power of two of rows that divides the
+// page size, at most 128; 32 rows of the contiguous cache), only boxes with a visible key, and
+// boxes whose page is bad are left out and marked.  A paged box is one copy: the tensor map splits
+// rows into groups of eight and their two 128-byte halves, so that the copy lays down whole
+// swizzle atoms [group][half][8 rows].  Small copies are bound by their number, not their bytes:
+// one copy for both halves of a 16-row page took the 32-sequence decode step (1.26 GB) from 275 to
+// 217 us, and four loading warps instead of one 32 sequences of 8K to 16K tokens at d 64 from 206
+// to 167 (pages of 16) and 327 to 225 (pages of 8); from pages of 32 rows on nothing of this
+// shows (6.4 TB/s at d 128, 5.7 at d 64).
+//
+// The softmax runs with one thread per key: its logits come with one TMEM load.  The running
 // maximum is common to the tile's keys and only moves when some logit exceeds it by 2^8 (one
 // barrier with an or-reduction tells); then O^T is rescaled in TMEM.  Row sums are kept per
 // thread and added up at the end of a segment.  V rows of keys that are not visible are zeroed
