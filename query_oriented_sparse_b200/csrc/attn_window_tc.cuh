@@ -15,7 +15,7 @@
 // exponentials take about the same time (1024 clocks each per block and SM, of the 2000 it
 // takes), and windows make tiles short, so starting and finishing a tile weighs as much as seven
 // blocks.  So every cluster runs two tiles at once, each with its own loader warp, MMA thread,
-// eight softmax warps, S and O in TMEM (S_x at columns 128 x, P over it; O_x at 256 + 128 x), Q
+// four softmax warps, S and O in TMEM (S_x at columns 128 x, P over it; O_x at 256 + 128 x), Q
 // buffer and rings of two K and two V stages, and the two only take turns at the tensor pipe: one
 // tile's start, end and masked blocks pass under the other's work.  Measured on 4096 queries of 32
 // heads, 8 KV heads, window 4096, d 128: 287 us (961 TFLOP/s); with one tile at a time whose
@@ -25,8 +25,7 @@
 // its two streams in turn; the last of an odd number both streams share by key blocks, and
 // stream 1's half reaches stream 0 through shared memory.
 //
-// Softmax: one thread per row and 64-key half of a block; the halves agree on the block's
-// maximum through shared memory.  The running maximum and sum are fp32; O is rescaled in TMEM
+// Softmax: one thread per row of a tile, all 128 keys of a block.  The running maximum and sum are fp32; O is rescaled in TMEM
 // only when the maximum grows by more than 2^8.  P is rounded to bf16 for its MMA (the row sum
 // is taken from the unrounded weights).
 //
@@ -40,8 +39,8 @@
 // When the tiles are fewer than the clusters (short chunks), each tile's blocks are split over
 // several units, which leave unnormalised partials (fp32) for the join kernel.
 //
-// Every mbarrier wait is bounded; the only unbounded waits are the cluster barriers and the
-// named barriers of a row's two halves, which every thread reaches on every path.
+// Every mbarrier wait is bounded; the only unbounded waits are the block's and the cluster's
+// barriers, which every thread reaches on every path.
 #pragma once
 #include <cooperative_groups.h>
 #include "attn_tc2.cuh"
@@ -49,7 +48,7 @@
 
 namespace quoka {
 
-constexpr int AWT_THREADS = 640;   // warps 0-1 load, 2-3 MMA, 4-11 and 12-19 softmax
+constexpr int AWT_THREADS = 384;   // warps 0-1 load, 2-3 MMA, 4-7 and 8-11 softmax
 constexpr int AWT_ST = 2;          // K stages, and V stages, per stream
 constexpr int AWT_BK = 128;        // keys per block
 
@@ -62,9 +61,8 @@ struct AwtCfg {
   static constexpr int H_BYTES = 16384;            // a CTA's share of a K or V block
   static constexpr int STREAM = Q_BYTES + 2 * AWT_ST * H_BYTES;
   static constexpr int BARS = 4 + 5 * AWT_ST;      // per stream
-  static constexpr int XBUF = 2 * 2 * 2 * 128 * 4; // [slot set][stream][half][row]
   static constexpr int MBUF = 2 * 128 * 4;         // a shared unit's (m, l) of stream 1
-  static constexpr int SMEM = 1024 + 2 * STREAM + (2 * BARS + 1) * 8 + 8 + 16 + 16 + XBUF + MBUF;
+  static constexpr int SMEM = 1024 + 2 * STREAM + (2 * BARS + 1) * 8 + 8 + 16 + 16 + MBUF;
 };
 
 // A unit of work: blocks [j0, j1) of the nblk blocks of a tile.
@@ -107,19 +105,19 @@ __device__ __forceinline__ WindowUnit window_unit(const WindowParams& p, const S
 }
 
 // Replaces by zero the values that are not finite in a thread's share of a V tile of 16 KB in
-// shared memory (thread tg of 256: the 16-byte vectors tg, tg + 256, ...).  Returns whether
+// shared memory (thread tg of 128: the 16-byte vectors tg, tg + 128, ...).  Returns whether
 // there were any.
 __device__ __forceinline__ bool window_clean_v(uint4* v, int tg) {
   uint32_t any = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {            // an exponent of ones carries into the sign's place
-    const uint4 x = v[i * 256 + tg];
+  for (int i = 0; i < 8; ++i) {            // an exponent of ones carries into the sign's place
+    const uint4 x = v[i * 128 + tg];
     any |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
            ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
   }
   if (!(any & 0x80008000u)) return false;
-  for (int i = 0; i < 4; ++i) {
-    uint32_t* w = reinterpret_cast<uint32_t*>(v + i * 256 + tg);
+  for (int i = 0; i < 8; ++i) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(v + i * 128 + tg);
     for (int k = 0; k < 4; ++k) {
       if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
       if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu;
@@ -183,7 +181,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = PAIR ? cluster.block_rank() : 0u;
   // this warp's stream, and that stream's memory
-  const int x = warp < 4 ? (warp & 1) : (warp - 4) >> 3;
+  const int x = warp < 4 ? (warp & 1) : (warp - 4) >> 2;
   uint8_t* sQ = smem + x * Cfg::STREAM;
   uint8_t* sK = sQ + Cfg::Q_BYTES;
   uint8_t* sV = sK + AWT_ST * Cfg::H_BYTES;
@@ -205,8 +203,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   // [stream][unit parity] unit number + 1 when a value of one of its cleaned V blocks was not finite
   volatile int* mark = reinterpret_cast<volatile int*>(tmem_slot + 4) + x * 2;
   int* turn = reinterpret_cast<int*>(tmem_slot) + 1;       // 1 while an MMA thread issues
-  float* xbuf = reinterpret_cast<float*>(tmem_slot + 8);
-  float* mbuf = xbuf + Cfg::XBUF / 4;      // [m, l][row]
+  float* mbuf = reinterpret_cast<float*>(tmem_slot + 8);   // [m, l][row]
   // [column][row] of stream 1's O of a shared unit: over its K and V stages, which are done by then
   float* obuf = reinterpret_cast<float*>(smem + Cfg::STREAM + Cfg::Q_BYTES);
 
@@ -243,11 +240,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     ptx::mbar_init(qfull, 1);
     ptx::mbar_init(qpeer, 1);
     ptx::mbar_init(qempty, 1);
-    ptx::mbar_init(pready, 8 * Cfg::CTAS);
+    ptx::mbar_init(pready, 4 * Cfg::CTAS);
     for (int s = 0; s < 5 * AWT_ST; ++s) ptx::mbar_init(&sfull[s], 1);   // through vpeer
     if (x == 0) {
       *turn = 0;
-      ptx::mbar_init(merge, 8);
+      ptx::mbar_init(merge, 4);
     }
     ptx::fence_mbar_init();
   }
@@ -416,11 +413,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           if (ok) ok = take();
           if (!ok) break;
           ptx::tc_fence_after();
-          // P: keys 0-63 in columns 0-31 of S, keys 64-127 in columns 96-127
+          // P: bf16 pairs in the first 64 columns of S
           const uint32_t b0 = v_lo + (uint32_t)((jg % AWT_ST) * (Cfg::H_BYTES >> 4));
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            const uint32_t a = s_t + (uint32_t)(k < 4 ? k * 8 : 96 + (k - 4) * 8);
+            const uint32_t a = s_t + (uint32_t)(k * 8);
             const uint32_t acc = (j > 0 || k > 0) ? 1u : 0u;
             if constexpr (PAIR) ptx::mma_bf16_ts_pair(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
             else ptx::mma_bf16_ts_lh(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
@@ -435,69 +432,48 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       }
     }
   } else {
-    // ---------------- softmax ----------------
-    const int half = ((warp - 4) >> 2) & 1;                 // key half of each block
+    // ---------------- softmax: one thread per row ----------------
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;                      // row of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    constexpr int DH = D / 2;
-    const uint32_t s_addr = tmem + lane_off + (uint32_t)(x * 128 + half * 64);
-    const uint32_t p_addr = tmem + lane_off + (uint32_t)(x * 128 + half * 96);
-    const uint32_t o_addr = tmem + lane_off + 256u + (uint32_t)(x * 128 + half * DH);
-    const int bar_id = 1 + x * 4 + quarter;
+    const uint32_t s_addr = tmem + lane_off + (uint32_t)(x * 128);
+    const uint32_t o_addr = tmem + lane_off + 256u + (uint32_t)(x * 128);
     const uint32_t pready_c0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(pready), 0) : 0u;
-    // the two halves of a row post their values and each combines both; slots alternate
-    // between two sets, so one barrier per exchange suffices
-    int xphase = 0;
-    auto exchange = [&](float v, bool is_max) -> float {
-      float* slot = xbuf + ((xphase & 1) * 2 + x) * 256 + r;
-      slot[half * 128] = v;
-      ptx::named_bar(bar_id, 64);
-      const float a0 = slot[0], a1 = slot[128];
-      ++xphase;
-      return is_max ? fmaxf(a0, a1) : a0 + a1;
-    };
     bool ok = true;
     int jg = 0;
-    // The two warps of a row take part in exactly one exchange per block and one at the end of
-    // each unit, whatever happens: after a failed (timed-out) wait a warp skips the work but
-    // keeps the exchanges.
-    for (int it = 0; it < my_units; ++it) {
+    for (int it = 0; it < my_units && ok; ++it) {
       const WindowUnit u = unit_at(it);
       const int pos = u.p_lo + (int)rank * p.TP + r % p.TP; // this row's position
       float m_run = -INFINITY, l_run = 0.f;
       for (int j = u.j0; j < u.j1; ++j, ++jg) {
-        if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&sfull[jg % AWT_ST], (uint32_t)(jg / AWT_ST) & 1u));
-        if (!ok) {
-          (void)exchange(0.f, true);
-          continue;
-        }
+        ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep<2>(&sfull[jg % AWT_ST], (uint32_t)(jg / AWT_ST) & 1u));
+        if (!ok) break;
         ptx::tc_fence_after();
-        float s[64];
+        float s[128];
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
+        for (int c = 0; c < 128; c += 32) {
           uint32_t w[32];
           ptx::tmem_ld32(s_addr + (uint32_t)c, w);
 #pragma unroll
           for (int i = 0; i < 32; ++i) s[c + i] = __uint_as_float(w[i]);
         }
         ptx::tmem_ld_wait();
-        const bool whole = u.whole(j, p.window, p.n_sink);
-        if (!whole) {
+        if (!u.whole(j, p.window, p.n_sink)) {
           const int k0 = u.start(j), kend = u.end(j);
-          // bits of this row and half: below min(kend, pos + 1), and at pos - window + 1 or
-          // later or below n_sink
-          const int b0 = k0 + half * 64;
-          const int hi = min(kend, pos + 1) - b0, lo = pos - p.window + 1 - b0, sk = p.n_sink - b0;
-          const uint32_t w0 = low_bits(hi) & (~low_bits(lo) | low_bits(sk));
-          const uint32_t w1 = low_bits(hi - 32) & (~low_bits(lo - 32) | low_bits(sk - 32));
+          // bits of this row: below min(kend, pos + 1), and at pos - window + 1 or later or below
+          // n_sink
+          const int hi = min(kend, pos + 1) - k0, lo = pos - p.window + 1 - k0, sk = p.n_sink - k0;
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
-            if (!(((c < 32 ? w0 : w1) >> (c & 31)) & 1u)) s[c] = -INFINITY;
-          // clean this CTA's share of the V tile before P.V reads it (the stream's 256 threads)
+          for (int c = 0; c < 128; c += 32) {
+            const uint32_t w = low_bits(hi - c) & (~low_bits(lo - c) | low_bits(sk - c));
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (!((w >> i) & 1u)) s[c + i] = -INFINITY;
+          }
+          // clean this CTA's share of the V tile before P.V reads it (the stream's 128 threads)
           ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&vfull[jg % AWT_ST], (uint32_t)(jg / AWT_ST) & 1u));
-          const int tg = ((warp - 4) & 7) * 32 + lane;
-          if (ok && window_clean_v(reinterpret_cast<uint4*>(sV + (jg % AWT_ST) * Cfg::H_BYTES), tg)) {
+          if (!ok) break;
+          if (window_clean_v(reinterpret_cast<uint4*>(sV + (jg % AWT_ST) * Cfg::H_BYTES), r)) {
             mark[it & 1] = it + 1;
             if constexpr (PAIR) {          // this CTA's columns are in the other's rows too
               const uint32_t far = ptx::mapa_shared(ptx::smem_u32(const_cast<int*>(mark + (it & 1))), rank ^ 1u);
@@ -511,15 +487,15 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         {
           float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
 #pragma unroll
-          for (int c = 4; c < 60; c += 8) {
+          for (int c = 4; c < 124; c += 8) {
             m0 = ptx::max3(m0, s[c], s[c + 1]);
             m1 = ptx::max3(m1, s[c + 2], s[c + 3]);
             m2 = ptx::max3(m2, s[c + 4], s[c + 5]);
             m3 = ptx::max3(m3, s[c + 6], s[c + 7]);
           }
-          m0 = ptx::max3(m0, s[60], s[61]);
-          m1 = ptx::max3(m1, s[62], s[63]);
-          mx = exchange(fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)), true);
+          m0 = ptx::max3(m0, s[124], s[125]);
+          m1 = ptx::max3(m1, s[126], s[127]);
+          mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
         }
         const float m_cand = mx * p.scale_log2;
         const bool grow = m_cand > m_run + AT2_RESCALE_LOG2 || (m_run == -INFINITY && m_cand > -INFINITY);
@@ -532,7 +508,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
         float ls[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
+        for (int c = 0; c < 128; c += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -541,14 +517,14 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             ls[i & 3] += p0 + p1;
             pk[i] = pack_bf16x2(p0, p1);
           }
-          ptx::tmem_st16(p_addr + (uint32_t)(c / 2), pk);
+          ptx::tmem_st16(s_addr + (uint32_t)(c / 2), pk);
         }
         l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
         if (j > u.j0 && __any_sync(0xffffffffu, grow)) {
           // O holds the unit's earlier blocks: S(j), which this warp has seen, was issued after
           // their P.V, and its commit covers them
 #pragma unroll
-          for (int c = 0; c < DH; c += 16) {
+          for (int c = 0; c < D; c += 16) {
             uint32_t w[16];
             ptx::tmem_ld16(o_addr + (uint32_t)c, w);
             ptx::tmem_ld_wait();
@@ -563,7 +539,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         // relaxed arrive: P and the rescaled O are TMEM stores already completed by
         // tcgen05.wait::st and ordered by the fence above; a release would stall the warp on
         // unrelated memory operations (the stores of the unit before)
-        if (ok && lane == 0) {
+        if (lane == 0) {
           if constexpr (PAIR) ptx::mbar_arrive_cluster_relaxed(pready_c0);
           else ptx::mbar_arrive(pready);
         }
@@ -572,7 +548,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       // every earlier MMA; the stage's next release needs this warp's next P)
       if (ok && u.j1 > u.j0)
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(&vempty[(jg - 1) % AWT_ST], (uint32_t)((jg - 1) / AWT_ST) & 1u));
-      const float l_row = exchange(ok ? l_run : 0.f, false);   // every pair member reaches this
+      if (!ok) break;
+      const float l_row = l_run;
       const bool sh = shared_unit(it);
       const bool dirty = mark[it & 1] == it + 1;
       const int hl = r / p.TP;
@@ -581,37 +558,36 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const int orow = hl < p.G && t < p.C ? (u.b * p.h_q + u.g * p.G + hl) * p.C + t : -1;
       float l_all = l_row;
       ptx::tc_fence_after();
-      if (sh && ok) {
+      if (sh) {
         // a shared unit: stream 1 leaves O, m and l, stream 0 joins them to its own
-        float* ob = obuf + half * DH * 128 + r;
+        float* ob = obuf + r;
         if (x == 1) {
-          for (int c = 0; c < (u.j1 > u.j0 ? DH : 0); c += 16) {
+          for (int c = 0; c < (u.j1 > u.j0 ? D : 0); c += 16) {
             uint32_t w[16];
             ptx::tmem_ld16(o_addr + (uint32_t)c, w);
             ptx::tmem_ld_wait();
             float y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) y[i] = __uint_as_float(w[i]);
-            if (dirty && orow >= 0) window_add_bad(y, v_cache + half * DH + c, u, pos, p.window, p.n_sink, D);
+            if (dirty && orow >= 0) window_add_bad(y, v_cache + c, u, pos, p.window, p.n_sink, D);
 #pragma unroll
             for (int i = 0; i < 16; ++i) ob[(c + i) * 128] = y[i];
           }
-          if (half == 0) {
-            mbuf[r] = m_run;
-            mbuf[128 + r] = l_row;
-          }
+          mbuf[r] = m_run;
+          mbuf[128 + r] = l_row;
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(merge);
           continue;                        // (the cluster's last unit)
         }
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep(merge, 0));
-        const float m1 = mbuf[r], l1 = ok ? mbuf[128 + r] : 0.f;
+        if (!ok) break;
+        const float m1 = mbuf[r], l1 = mbuf[128 + r];
         const float M = l1 != 0.f ? (l_row != 0.f ? fmaxf(m_run, m1) : m1) : m_run;
         const float f0 = l_row != 0.f ? ptx::ex2_approx(m_run - M) : 0.f;
         const float f1 = l1 != 0.f ? ptx::ex2_approx(m1 - M) : 0.f;
         l_all = (l_row != 0.f ? l_row * f0 : 0.f) + (l1 != 0.f ? l1 * f1 : 0.f);
         m_run = M;
-        for (int c = 0; c < (ok && u.j1 > u.j0 ? DH : 0); c += 16) {   // (stream 0 has blocks when stream 1 has)
+        for (int c = 0; c < (u.j1 > u.j0 ? D : 0); c += 16) {   // (stream 0 has blocks when stream 1 has)
           uint32_t w[16];
           ptx::tmem_ld16(o_addr + (uint32_t)c, w);
           ptx::tmem_ld_wait();
@@ -624,17 +600,17 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         }
         ptx::tmem_st_wait();
       }
-      if (ok) {
+      {
         const bool split = p.nsplit > 1;
         // split units leave O and (m, l); others every row's O / l (each sees its own key)
         const float inv_l = split ? 1.f : 1.f / l_all;
         const size_t prow = ((size_t)(cid + (2 * it + (sh ? 0 : x)) * ncl) * Cfg::CTAS + rank) * 128 + r;
-        if (split && half == 0) {
+        if (split) {
           p.part_ml[prow * 2] = m_run;
           p.part_ml[prow * 2 + 1] = l_all;
         }
 #pragma unroll
-        for (int c = 0; c < (u.j1 > u.j0 ? DH : 0); c += 32) {
+        for (int c = 0; c < (u.j1 > u.j0 ? D : 0); c += 32) {
           uint4 w4[4];                     // 32 output columns as bf16
 #pragma unroll
           for (int cc = 0; cc < 32; cc += 16) {
@@ -648,12 +624,12 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
               float y[16];                 // (its address is taken here alone: o stays in registers)
 #pragma unroll
               for (int i = 0; i < 16; ++i) y[i] = o[i];
-              window_add_bad(y, v_cache + half * DH + c + cc, u, pos, p.window, p.n_sink, D);
+              window_add_bad(y, v_cache + c + cc, u, pos, p.window, p.n_sink, D);
 #pragma unroll
               for (int i = 0; i < 16; ++i) o[i] = y[i];
             }
             if (split) {
-              float4* d4 = reinterpret_cast<float4*>(p.part + prow * D + half * DH + c + cc);
+              float4* d4 = reinterpret_cast<float4*>(p.part + prow * D + c + cc);
               if (orow >= 0) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) d4[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
@@ -675,7 +651,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
             for (int i = 0; i < 4; ++i) {
               const int row = __shfl_sync(0xffffffffu, orow, (lane & ~3) + i);
               if (row >= 0)
-                reinterpret_cast<uint4*>(out + (size_t)row * D + half * DH + c)[lane & 3] = w4[i];
+                reinterpret_cast<uint4*>(out + (size_t)row * D + c)[lane & 3] = w4[i];
             }
           }
         }

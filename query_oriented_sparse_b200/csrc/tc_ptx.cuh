@@ -92,8 +92,9 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
 }
 // As mbar_wait: a few plain tries first (a phase about to complete is seen without a
 // wake-up delay), then each try sleeps until the phase completes (or 1 ms passes).
+template <int kTries = 16>
 __device__ __forceinline__ bool mbar_wait_sleep(uint64_t* bar, uint32_t parity) {
-  for (int i = 0; i < 16; ++i)
+  for (int i = 0; i < kTries; ++i)
     if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer();
   for (;;) {
