@@ -506,20 +506,21 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           l_run *= alpha;
         }
         const float m_use = (m_run == -INFINITY) ? 0.f : m_run;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), minus_m2 = make_float2(-m_use, -m_use);
+        float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const float p0 = ptx::ex2_approx(fmaf(s[c + 2 * i], p.scale_log2, -m_use));
-            const float p1 = ptx::ex2_approx(fmaf(s[c + 2 * i + 1], p.scale_log2, -m_use));
-            ls[i & 3] += p0 + p1;
-            pk[i] = pack_bf16x2(p0, p1);
+            const float2 t = ptx::fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), scale2, minus_m2);
+            const float2 e = make_float2(ptx::ex2_approx(t.x), ptx::ex2_approx(t.y));
+            l2[i & 1] = ptx::add2(l2[i & 1], e);
+            pk[i] = pack_bf16x2(e.x, e.y);
           }
           ptx::tmem_st16(s_addr + (uint32_t)(c / 2), pk);
         }
-        l_run += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l_run += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         if (j > u.j0 && __any_sync(0xffffffffu, grow)) {
           // O holds the unit's earlier blocks: S(j), which this warp has seen, was issued after
           // their P.V, and its commit covers them
@@ -609,17 +610,19 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           p.part_ml[prow * 2] = m_run;
           p.part_ml[prow * 2 + 1] = l_all;
         }
+        if (u.j0 == u.j1) continue;        // (a unit without blocks: O is not set)
+        uint32_t w[2][32];                 // the next 32 columns are on their way while these are stored
+        ptx::tmem_ld32(o_addr, w[0]);
 #pragma unroll
-        for (int c = 0; c < (u.j1 > u.j0 ? D : 0); c += 32) {
+        for (int c = 0; c < D; c += 32) {
+          ptx::tmem_ld_wait();
+          if (c + 32 < D) ptx::tmem_ld32(o_addr + (uint32_t)(c + 32), w[(c / 32 + 1) & 1]);
           uint4 w4[4];                     // 32 output columns as bf16
 #pragma unroll
           for (int cc = 0; cc < 32; cc += 16) {
-            uint32_t w[16];
-            ptx::tmem_ld16(o_addr + (uint32_t)(c + cc), w);
-            ptx::tmem_ld_wait();
             float o[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[i]) * inv_l;
+            for (int i = 0; i < 16; ++i) o[i] = __uint_as_float(w[(c / 32) & 1][cc + i]) * inv_l;
             if (dirty && orow >= 0) {
               float y[16];                 // (its address is taken here alone: o stays in registers)
 #pragma unroll
