@@ -11,9 +11,9 @@
 // CTA holds whole is finished there; one that several share leaves at most one partial
 // (running maximum, sum and output, fp32) per CTA, two slots in all, and the join kernel
 // merges them.  Where the sequences are short (four tiles at most), a CTA takes a (sequence,
-// KV head) whole instead, and there is nothing to join: one launch.  With a weight record, the logits are kept (fp32, base 2) and the record
-// kernel adds each key's softmax weight, summed over the group's heads, once the join has
-// the row's maximum and sum.
+// KV head) whole instead, and there is nothing to join: one launch.  With a weight record,
+// the logits are kept (fp32, base 2) and the record kernel adds each key's softmax weight,
+// summed over the group's heads, once the join has the row's maximum and sum.
 //
 // This file: the split, the CUDA-core kernel (fp32), the join and the record kernel.  fp32 with
 // one head to a group reads at 5.8 TB/s (d 128, 16 sequences of 4K to 8K tokens); more heads
@@ -26,7 +26,6 @@
 namespace quoka {
 
 constexpr int AST_TILE = 128;             // keys per tile
-constexpr int AST_MAX_BATCH = 1024;
 
 // Visible key tiles of one sequence: nst tiles of first tokens, then tiles wt0 onwards.
 struct KeySpan {
@@ -281,11 +280,9 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
         const float mn = fmaxf(m[r], mx);
-        float pr = 0.f, corr = 1.f;
-        if (mn != -INFINITY) {
-          pr = exp2f(sc[r] - mn);
-          corr = exp2f(m[r] - mn);
-        }
+        // (a maximum of -inf: the keys so far are masked and weigh 0, or NaN, which stays)
+        const float pr = exp2f(sc[r] - (mn == -INFINITY ? 0.f : mn));
+        const float corr = mn == -INFINITY ? 1.f : exp2f(m[r] - mn);
         float sum = pr;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);

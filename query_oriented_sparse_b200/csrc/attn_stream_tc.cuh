@@ -395,8 +395,8 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           if (r >= rows) break;
-          // (a row whose keys so far are all masked has m = -inf and weights 0)
-          const float pr = m[r] == -INFINITY ? 0.f : ptx::ex2_approx(s[r] - m[r]);
+          // (m = -inf: the row's keys so far are masked, s = -inf, and weigh 0, or NaN, which stays)
+          const float pr = ptx::ex2_approx(s[r] - (m[r] == -INFINITY ? 0.f : m[r]));
           l[r] += pr;
           *reinterpret_cast<__nv_bfloat16*>(p_key + buf * Cfg::P_BYTES + r * 128 + ((p_chunk ^ (r & 7)) << 4)) =
               __float2bfloat16_rn(pr);

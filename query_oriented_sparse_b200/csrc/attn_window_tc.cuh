@@ -18,16 +18,17 @@
 // four softmax warps, S and O in TMEM (S_x at columns 128 x, P over it; O_x at 256 + 128 x), Q
 // buffer and rings of two K and two V stages, and the two only take turns at the tensor pipe: one
 // tile's start, end and masked blocks pass under the other's work.  Measured on 4096 queries of 32
-// heads, 8 KV heads, window 4096, d 128: 287 us (961 TFLOP/s); with one tile at a time whose
-// blocks the two softmax groups share, as in attn_tc2.cuh, 320; without the turns 430.  8
-// sequences of 1024 queries, 16 heads to a KV head, window 2047: 628 us against 796.
+// heads, 8 KV heads, window 4096, d 128: 280 us (983 TFLOP/s; 310 when repeated for long, under the
+// power limit); with one tile at a time whose blocks the two softmax groups share, as in
+// attn_tc2.cuh, 320; without the turns 430.  8 sequences of 1024 queries, 16 heads to a KV head,
+// window 2047: 616 us against 796.
 // The clusters resident at once walk the tile list, cluster c taking tiles c, c + N, ...,
 // its two streams in turn; the last of an odd number both streams share by key blocks, and
 // stream 1's half reaches stream 0 through shared memory.
 //
-// Softmax: one thread per row of a tile, all 128 keys of a block.  The running maximum and sum are fp32; O is rescaled in TMEM
-// only when the maximum grows by more than 2^8.  P is rounded to bf16 for its MMA (the row sum
-// is taken from the unrounded weights).
+// Softmax: one thread per row of a tile, all 128 keys of a block.  The running maximum and sum
+// are fp32; O is rescaled in TMEM only when the maximum grows by more than 2^8.  P is rounded to
+// bf16 for its MMA (the row sum is taken from the unrounded weights).
 //
 // A block that not every row sees whole (the diagonal, the window's lower edge, the end of the
 // first tokens) is masked by selection.  Its V tile is searched first for values that are not

@@ -224,6 +224,21 @@ def test_decode_visible_bad_values_are_passed_on(dtype, bad, cuda_device):
     assert torch.isfinite(out[0, 4:, 0, :9].float()).all() and torch.isfinite(out[0, 4:, 0, 10:].float()).all()
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("n", [100, 3000])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_decode_bad_query_is_its_own_affair(dtype, n, cuda_device):
+    pool = Pool(2, 128, 16, (n, n), dtype, seed=40)
+    q = torch.randn(2, 8, 1, 128, generator=torch.Generator().manual_seed(41)).to(dtype)
+    good, _ = run_decode(pool, q)
+    q2 = q.clone()
+    q2[0, 6, 0, 100] = float("nan")
+    out, _ = run_decode(pool, q2)
+    assert out[0, 6].isnan().all()
+    out[0, 6] = good[0, 6]
+    assert torch.equal(out, good)
+
+
 # ---- append -----------------------------------------------------------------------------
 
 @pytest.mark.gpu

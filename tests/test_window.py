@@ -155,6 +155,23 @@ def test_bad_rows_reach_only_their_readers(d, dtype, bad, cuda_device):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("C", [1, 70])
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_bad_query_is_its_own_affair(d, dtype, C, cuda_device):
+    """A query that holds NaN gives NaN, and no other row changes."""
+    prefix = (300, 41)
+    q, k, v, off = make(8, 2, d, C, prefix, dtype, seed=9)
+    clean = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), off, prefix, 200, 3).cpu()
+    q2 = q.clone()
+    q2[1, 5, C // 2, 3] = float("nan")
+    out = Bd.window_chunk_attn(q2.cuda(), k.cuda(), v.cuda(), off, prefix, 200, 3).cpu()
+    assert out[1, 5, C // 2].isnan().all()
+    out[1, 5, C // 2] = clean[1, 5, C // 2]
+    assert torch.equal(out, clean)
+
+
+@pytest.mark.gpu
 def test_all_keys_equal_selecting_every_key(cuda_device):
     """A window over everything is the attention of sparse_chunk_attn with every prefix key."""
     prefix, C = (500, 77), 140
