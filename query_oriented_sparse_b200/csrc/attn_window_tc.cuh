@@ -7,26 +7,28 @@
 // two CTAs, 2 TP positions, 256-row tcgen05 MMAs with cta_group::2, each SM holding half of
 // every K and V block), d = 64 on single SMs, whose K and V blocks are half the size.  K and V
 // come straight from the cache by TMA: the keys of a tile are one run of rows after the first
-// tokens, and blocks of 128 keys start at the oldest key that the tile's first position sees,
+// tokens, and blocks of 64 keys start at the oldest key that the tile's first position sees,
 // so a tile walks the fewest blocks.  Tiles of neighbouring positions run at the same time and
 // share most of their keys in L2.
 //
-// What bounds it is the chain S = Q K^T -> softmax -> O += P V of each tile: tensor cores and
-// exponentials take about the same time (1024 clocks each per block and SM, of the 2000 it
-// takes), and windows make tiles short, so starting and finishing a tile weighs as much as seven
-// blocks.  So every cluster runs two tiles at once, each with its own loader warp, MMA thread,
-// four softmax warps, S and O in TMEM (S_x at columns 128 x, P over it; O_x at 256 + 128 x), Q
-// buffer and rings of two K and two V stages, and the two only take turns at the tensor pipe: one
-// tile's start, end and masked blocks pass under the other's work.  Measured on 4096 queries of 32
-// heads, 8 KV heads, window 4096, d 128: 280 us (983 TFLOP/s; 310 when repeated for long, under the
-// power limit); with one tile at a time whose blocks the two softmax groups share, as in
-// attn_tc2.cuh, 320; without the turns 430.  8 sequences of 1024 queries, 16 heads to a KV head,
-// window 2047: 616 us against 796.
+// What bounds it is the softmax of the tiles: exponentials and products would each take 512
+// clocks per block of 64 keys and SM, and windows make tiles short, so starting and finishing a
+// tile weighs as much as ten blocks.  So every cluster runs two tiles at once, each with its own
+// loader warp, MMA thread, four softmax warps, O in TMEM (columns 256 + 128 x), two buffers of S
+// (columns 128 x and 128 x + 64, P over S), Q buffer and rings of four K and four V stages: one
+// tile's start, end and masked blocks pass under the other's work.  S of block j + 2 is issued
+// behind P.V of block j, so a softmax warp finds the next S done while its last block's products
+// run.  A block then takes about 850 clocks per SM.  Measured on 4096 queries of 32 heads, 8 KV
+// heads, window 4096, d 128: 266 us (1034 TFLOP/s).
+// With blocks of 128 keys, which leave TMEM for one S per tile, so that each tile's products and
+// softmax wait for one another, 280; with one tile at a time whose blocks the two softmax groups
+// share, as in attn_tc2.cuh, 320.  8 sequences of 1024 queries, 16 heads to a KV head, window
+// 2047: 549 us against 616 with blocks of 128 keys.
 // The clusters resident at once walk the tile list, cluster c taking tiles c, c + N, ...,
 // its two streams in turn; the last of an odd number both streams share by key blocks, and
 // stream 1's half reaches stream 0 through shared memory.
 //
-// Softmax: one thread per row of a tile, all 128 keys of a block.  The running maximum and sum
+// Softmax: one thread per row of a tile, all 64 keys of a block.  The running maximum and sum
 // are fp32; O is rescaled in TMEM only when the maximum grows by more than 2^8.  P is rounded to
 // bf16 for its MMA (the row sum is taken from the unrounded weights).
 //
@@ -50,8 +52,8 @@
 namespace quoka {
 
 constexpr int AWT_THREADS = 384;   // warps 0-1 load, 2-3 MMA, 4-7 and 8-11 softmax
-constexpr int AWT_ST = 2;          // K stages, and V stages, per stream
-constexpr int AWT_BK = 128;        // keys per block
+constexpr int AWT_ST = 4;          // K stages, and V stages, per stream
+constexpr int AWT_BK = 64;         // keys per block
 
 template <int D>
 struct AwtCfg {
@@ -59,9 +61,9 @@ struct AwtCfg {
   static constexpr int CTAS = PAIR ? 2 : 1;        // CTAs per cluster
   static constexpr int KB = D / 64;
   static constexpr int Q_BYTES = 128 * D * 2;      // a CTA's query tile
-  static constexpr int H_BYTES = 16384;            // a CTA's share of a K or V block
+  static constexpr int H_BYTES = 8192;             // a CTA's share of a K or V block
   static constexpr int STREAM = Q_BYTES + 2 * AWT_ST * H_BYTES;
-  static constexpr int BARS = 4 + 5 * AWT_ST;      // per stream
+  static constexpr int BARS = 5 + 5 * AWT_ST;      // per stream
   static constexpr int MBUF = 2 * 128 * 4;         // a shared unit's (m, l) of stream 1
   static constexpr int SMEM = 1024 + 2 * STREAM + (2 * BARS + 1) * 8 + 8 + 16 + 16 + MBUF;
 };
@@ -98,26 +100,26 @@ __device__ __forceinline__ WindowUnit window_unit(const WindowParams& p, const S
   u.w0 = s.w0;
   u.nsb = (s.ns + AWT_BK - 1) / AWT_BK;
   const int nblk = u.nsb + (s.p1 - s.w0) / AWT_BK + 1;
-  const unsigned sp = (unsigned)unit - tile * p.nsplit;    // nblk < 2^24 and nsplit <= 32
+  const unsigned sp = (unsigned)unit - tile * p.nsplit;    // nblk <= 2^25 and nsplit <= 32
   u.j0 = (int)(nblk * sp / (unsigned)p.nsplit);
   u.j1 = (int)(nblk * (sp + 1) / (unsigned)p.nsplit);
   u.row0 = (long long)u.g * p.rows_per_head + tab.kv_off[u.b];
   return u;
 }
 
-// Replaces by zero the values that are not finite in a thread's share of a V tile of 16 KB in
+// Replaces by zero the values that are not finite in a thread's share of a V tile of 8 KB in
 // shared memory (thread tg of 128: the 16-byte vectors tg, tg + 128, ...).  Returns whether
 // there were any.
 __device__ __forceinline__ bool window_clean_v(uint4* v, int tg) {
   uint32_t any = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {            // an exponent of ones carries into the sign's place
+  for (int i = 0; i < 4; ++i) {            // an exponent of ones carries into the sign's place
     const uint4 x = v[i * 128 + tg];
     any |= ((x.x & 0x7F807F80u) + 0x00800080u) | ((x.y & 0x7F807F80u) + 0x00800080u) |
            ((x.z & 0x7F807F80u) + 0x00800080u) | ((x.w & 0x7F807F80u) + 0x00800080u);
   }
   if (!(any & 0x80008000u)) return false;
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     uint32_t* w = reinterpret_cast<uint32_t*>(v + i * 128 + tg);
     for (int k = 0; k < 4; ++k) {
       if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
@@ -190,10 +192,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   uint64_t* qfull = bars;                  // this CTA's query tile landed
   uint64_t* qpeer = bars + 1;              // (CTA 0) CTA 1's query tile landed
   uint64_t* qempty = bars + 2;             // the S MMAs reading it are done (both CTAs)
-  uint64_t* pready = bars + 3;             // CTA 0: the pair's softmax warps of the stream wrote P
-  // [block parity], both CTAs: S of the block is done, and with it every MMA before; its K
-  // stage is free then
-  uint64_t* sfull = bars + 4;
+  uint64_t* pready = bars + 3;             // [block parity], CTA 0: the pair's softmax warps of the stream wrote P
+  // [stage], both CTAs: S of the block is done, and with it every MMA before; its K stage is
+  // free then
+  uint64_t* sfull = bars + 5;
   uint64_t* vempty = sfull + AWT_ST;       // [stage], both CTAs: P.V of the block is done
   uint64_t* kfull = vempty + AWT_ST;       // [stage], CTA 0: the K bytes of both CTAs
   uint64_t* vfull = kfull + AWT_ST;        // [stage], this CTA's V bytes
@@ -203,7 +205,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(end_bars + 2);
   // [stream][unit parity] unit number + 1 when a value of one of its cleaned V blocks was not finite
   volatile int* mark = reinterpret_cast<volatile int*>(tmem_slot + 4) + x * 2;
-  int* turn = reinterpret_cast<int*>(tmem_slot) + 1;       // 1 while an MMA thread issues
   float* mbuf = reinterpret_cast<float*>(tmem_slot + 8);   // [m, l][row]
   // [column][row] of stream 1's O of a shared unit: over its K and V stages, which are done by then
   float* obuf = reinterpret_cast<float*>(smem + Cfg::STREAM + Cfg::Q_BYTES);
@@ -241,12 +242,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     ptx::mbar_init(qfull, 1);
     ptx::mbar_init(qpeer, 1);
     ptx::mbar_init(qempty, 1);
-    ptx::mbar_init(pready, 4 * Cfg::CTAS);
+    for (int s = 0; s < 2; ++s) ptx::mbar_init(&pready[s], 4 * Cfg::CTAS);
     for (int s = 0; s < 5 * AWT_ST; ++s) ptx::mbar_init(&sfull[s], 1);   // through vpeer
-    if (x == 0) {
-      *turn = 0;
-      ptx::mbar_init(merge, 4);
-    }
+    if (x == 0) ptx::mbar_init(merge, 4);
     ptx::fence_mbar_init();
   }
   if (warp == 2) {
@@ -289,7 +287,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
               const uint32_t fbar = ptx::mapa_shared(ptx::smem_u32(&kfull[st]), 0);
 #pragma unroll
               for (int kb = 0; kb < 2; ++kb)
-                ptx::tma_load_2d_pair(k_st + kb * 8192, &kmap, fbar, kb * 64, row + 64 * (int)rank);
+                ptx::tma_load_2d_pair(k_st + kb * 4096, &kmap, fbar, kb * 64, row + 32 * (int)rank);
             } else {
               ptx::mbar_expect_tx(&kfull[st], (uint32_t)Cfg::H_BYTES);
               ptx::tma_load_2d(k_st, &kmap, &kfull[st], 0, row);
@@ -361,14 +359,15 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const uint32_t s_t = tmem + (uint32_t)(x * 128), o_t = tmem + 256u + (uint32_t)(x * 128);
       auto s_mmas = [&](int jj) {
         const uint32_t b0 = k_lo + (uint32_t)((jj % AWT_ST) * (Cfg::H_BYTES >> 4));
+        const uint32_t s_b = s_t + (uint32_t)((jj & 1) * AWT_BK);
 #pragma unroll
         for (int kb = 0; kb < Cfg::KB; ++kb)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t a = q_lo + (uint32_t)(kb * 1024 + k * 2);
-            const uint32_t bb = b0 + (uint32_t)(kb * 512 + k * 2);
-            if constexpr (PAIR) ptx::mma_bf16_ss_pair(s_t, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
-            else ptx::mma_bf16_ss_lh(s_t, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
+            const uint32_t bb = b0 + (uint32_t)(kb * 256 + k * 2);
+            if constexpr (PAIR) ptx::mma_bf16_ss_pair(s_b, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
+            else ptx::mma_bf16_ss_lh(s_b, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
           }
       };
       auto k_landed = [&](int jj) { return wait_pair(&kfull[jj % AWT_ST], (uint32_t)(jj / AWT_ST) & 1u); };
@@ -377,19 +376,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         return ptx::mbar_wait_sleep(&vfull[jj % AWT_ST], ph) &&
                (!PAIR || ptx::mbar_wait_cluster_sleep(&vpeer[jj % AWT_ST], ph));
       };
-      // The two threads issue a block's MMAs in one run each, by turns.  Interleaved in the tensor
-      // pipe, both streams would wait for both runs, and their softmax then run at the same time.
-      auto take = [&]() -> bool {
-        if (atomicExch(turn, 1) == 0) return true;
-        const uint64_t t0 = ptx::globaltimer();
-        for (uint32_t i = 1; atomicExch(turn, 1) != 0; ++i)
-          if ((i & 255u) == 0 && ptx::globaltimer() - t0 > ptx::kWaitLimitNs) {
-            flag_error(ERR_WAIT_TIMEOUT);
-            return false;
-          }
-        return true;
-      };
-      auto give = [&]() { *reinterpret_cast<volatile int*>(turn) = 0; };
       bool ok = true;
       int jg = 0, uq = 0;
       for (int it = 0; it < my_units && ok; ++it) {
@@ -398,36 +384,36 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         if (n == 0) continue;
         ok = ptx::mbar_wait_sleep(qfull, (uint32_t)uq & 1u);
         if (PAIR && ok) ok = ptx::mbar_wait_cluster_sleep(qpeer, (uint32_t)uq & 1u);
-        if (ok) ok = k_landed(jg);
-        if (!ok) break;
-        ok = take();
-        if (!ok) break;
-        ptx::tc_fence_after();
-        s_mmas(jg);
-        give();
-        commit(&sfull[jg % AWT_ST]);
-        if (n == 1) commit(qempty);
-        // every wait of a block comes before its MMAs, which are issued back to back
-        for (int j = 0; j < n && ok; ++j, ++jg) {
-          const bool more = j + 1 < n;
-          ok = v_landed(jg) && (!more || k_landed(jg + 1)) && wait_pair(pready, (uint32_t)jg & 1u);
-          if (ok) ok = take();
+        for (int j = 0; j < min(n, 2) && ok; ++j) {
+          ok = k_landed(jg + j);
           if (!ok) break;
           ptx::tc_fence_after();
-          // P: bf16 pairs in the first 64 columns of S
+          s_mmas(jg + j);
+          commit(&sfull[(jg + j) % AWT_ST]);
+        }
+        if (!ok) break;
+        if (n <= 2) commit(qempty);
+        // every wait of a block comes before its MMAs, which are issued back to back
+        for (int j = 0; j < n && ok; ++j, ++jg) {
+          const bool more = j + 2 < n;
+          ok = v_landed(jg) && (!more || k_landed(jg + 2)) && wait_pair(&pready[jg & 1], (uint32_t)(jg >> 1) & 1u);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          // P: bf16 pairs in the first 32 columns of S
           const uint32_t b0 = v_lo + (uint32_t)((jg % AWT_ST) * (Cfg::H_BYTES >> 4));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t a = s_t + (uint32_t)(k * 8);
+          for (int k = 0; k < AWT_BK / 16; ++k) {
+            const uint32_t a = s_t + (uint32_t)((jg & 1) * AWT_BK + k * 8);
             const uint32_t acc = (j > 0 || k > 0) ? 1u : 0u;
             if constexpr (PAIR) ptx::mma_bf16_ts_pair(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
             else ptx::mma_bf16_ts_lh(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
           }
-          if (more) s_mmas(jg + 1);        // over P: after P.V has read it (issued in order)
-          give();
-          if (more) commit(&sfull[(jg + 1) % AWT_ST]);
           commit(&vempty[jg % AWT_ST]);
-          if (j + 2 == n) commit(qempty);  // the unit's last S: its query buffer is free
+          if (more) {
+            s_mmas(jg + 2);                // over P: after P.V has read it (issued in order)
+            commit(&sfull[(jg + 2) % AWT_ST]);
+          }
+          if (j + 3 == n) commit(qempty);  // the unit's last S: its query buffer is free
         }
         ++uq;
       }
@@ -437,7 +423,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     const int quarter = warp & 3;
     const int r = quarter * 32 + lane;                      // row of the tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t s_addr = tmem + lane_off + (uint32_t)(x * 128);
+    const uint32_t s_addr0 = tmem + lane_off + (uint32_t)(x * 128);
     const uint32_t o_addr = tmem + lane_off + 256u + (uint32_t)(x * 128);
     const uint32_t pready_c0 = PAIR ? ptx::mapa_shared(ptx::smem_u32(pready), 0) : 0u;
     bool ok = true;
@@ -450,9 +436,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep<2>(&sfull[jg % AWT_ST], (uint32_t)(jg / AWT_ST) & 1u));
         if (!ok) break;
         ptx::tc_fence_after();
-        float s[128];
+        const uint32_t s_addr = s_addr0 + (uint32_t)((jg & 1) * AWT_BK);
+        float s[AWT_BK];
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < AWT_BK; c += 32) {
           uint32_t w[32];
           ptx::tmem_ld32(s_addr + (uint32_t)c, w);
 #pragma unroll
@@ -465,7 +452,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           // n_sink
           const int hi = min(kend, pos + 1) - k0, lo = pos - p.window + 1 - k0, sk = p.n_sink - k0;
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) {
+          for (int c = 0; c < AWT_BK; c += 32) {
             const uint32_t w = low_bits(hi - c) & (~low_bits(lo - c) | low_bits(sk - c));
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -488,14 +475,14 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         {
           float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
 #pragma unroll
-          for (int c = 4; c < 124; c += 8) {
+          for (int c = 4; c < AWT_BK - 4; c += 8) {
             m0 = ptx::max3(m0, s[c], s[c + 1]);
             m1 = ptx::max3(m1, s[c + 2], s[c + 3]);
             m2 = ptx::max3(m2, s[c + 4], s[c + 5]);
             m3 = ptx::max3(m3, s[c + 6], s[c + 7]);
           }
-          m0 = ptx::max3(m0, s[124], s[125]);
-          m1 = ptx::max3(m1, s[126], s[127]);
+          m0 = ptx::max3(m0, s[AWT_BK - 4], s[AWT_BK - 3]);
+          m1 = ptx::max3(m1, s[AWT_BK - 2], s[AWT_BK - 1]);
           mx = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3));
         }
         const float m_cand = mx * p.scale_log2;
@@ -510,7 +497,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         const float2 scale2 = make_float2(p.scale_log2, p.scale_log2), minus_m2 = make_float2(-m_use, -m_use);
         float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 128; c += 32) {
+        for (int c = 0; c < AWT_BK; c += 32) {
           uint32_t pk[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
@@ -523,8 +510,12 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         }
         l_run += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
         if (j > u.j0 && __any_sync(0xffffffffu, grow)) {
-          // O holds the unit's earlier blocks: S(j), which this warp has seen, was issued after
-          // their P.V, and its commit covers them
+          // O holds the unit's earlier blocks once the P.V of the one before is done (this block's
+          // waits for this warp)
+          ok = __all_sync(0xffffffffu, ptx::mbar_wait_sleep<2>(&vempty[(jg - 1) % AWT_ST],
+                                                               (uint32_t)((jg - 1) / AWT_ST) & 1u));
+          if (!ok) break;
+          ptx::tc_fence_after();
 #pragma unroll
           for (int c = 0; c < D; c += 16) {
             uint32_t w[16];
@@ -542,8 +533,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         // tcgen05.wait::st and ordered by the fence above; a release would stall the warp on
         // unrelated memory operations (the stores of the unit before)
         if (lane == 0) {
-          if constexpr (PAIR) ptx::mbar_arrive_cluster_relaxed(pready_c0);
-          else ptx::mbar_arrive(pready);
+          if constexpr (PAIR) ptx::mbar_arrive_cluster_relaxed(pready_c0 + (uint32_t)(jg & 1) * 8u);
+          else ptx::mbar_arrive(&pready[jg & 1]);
         }
       }
       // epilogue: O is final once the unit's last P.V has released its stage (that commit covers

@@ -257,7 +257,7 @@ StreamWs window_ws(const Dims& d, int max_prefix) { return stream_ws(d, (long lo
 // (rows / G) positions: bf16 d 128 two CTAs of 128 rows, bf16 d 64 one, fp32 one of 64 rows.
 constexpr int WINDOW_PAIRS = 74;              // bf16, d 128: clusters of two SMs, whose two streams share a unit
 constexpr int WINDOW_SINGLES = 148;           // bf16, d 64; fp32
-constexpr int WINDOW_MIN_BLOCKS = 8;          // 128-key (fp32: 64-key) blocks per unit at least
+constexpr int WINDOW_MIN_BLOCKS = 8;          // 64-key blocks per unit at least
 constexpr int WINDOW_MAX_SPLIT = 32;
 
 struct WindowWs {

@@ -311,3 +311,34 @@ def test_binding_refuses_strides_shapes_and_types():
         a.update(bad)
         with pytest.raises(Bd.QuokaError):
             Bd.window_chunk_attn(a["q"], a["k"], a["v"], a["off"], (92,), 10)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_bad_key_reaches_every_reader(d, dtype, cuda_device):
+    """A K row that holds NaN makes the rows that see it NaN, whichever of a block's keys it is."""
+    prefix, window, C = (300,), 90, 130
+    q, k, v, off = make(8, 2, d, C, prefix, dtype, seed=11)
+    clean = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), off, prefix, window, 0).cpu()
+    for u in range(16):
+        k2 = k.clone()
+        k2[:, 300 + 20 + u, 7] = float("nan")
+        out = Bd.window_chunk_attn(q.cuda(), k2.cuda(), v.cuda(), off, prefix, window, 0).cpu()
+        t = torch.arange(C)
+        sees = (t >= 20 + u) & (t - 20 - u < window)
+        assert out[0][:, sees].isnan().all()
+        assert torch.equal(out[0][:, ~sees], clean[0][:, ~sees])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1e-3, 8.0, 40.0])
+def test_flat_and_peaked_rows(scale, d, dtype, cuda_device):
+    """From weights that are all alike to ones that leave the range of fp32."""
+    prefix, window, n_sink, C = (500, 0), 333, 4, 200
+    q, k, v, off = make(8, 2, d, C, prefix, dtype, seed=12)
+    q = (scale * q.double()).to(dtype)
+    out = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), off, prefix, window, n_sink).cpu()
+    check(q, k, v, off, prefix, window, n_sink, out)
