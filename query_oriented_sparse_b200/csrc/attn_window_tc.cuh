@@ -14,16 +14,17 @@
 // What bounds it is the softmax of the tiles: exponentials and products would each take 512
 // clocks per block of 64 keys and SM, and windows make tiles short, so starting and finishing a
 // tile weighs as much as ten blocks.  So every cluster runs two tiles at once, each with its own
-// loader warp, MMA thread, four softmax warps, O in TMEM (columns 256 + 128 x), two buffers of S
+// loader warp, MMA warp, four softmax warps, O in TMEM (columns 256 + 128 x), two buffers of S
 // (columns 128 x and 128 x + 64, P over S), Q buffer and rings of four K and four V stages: one
 // tile's start, end and masked blocks pass under the other's work.  S of block j + 2 is issued
 // behind P.V of block j, so a softmax warp finds the next S done while its last block's products
 // run.  A block then takes about 850 clocks per SM.  Measured on 4096 queries of 32 heads, 8 KV
-// heads, window 4096, d 128: 266 us (1034 TFLOP/s).
+// heads, window 4096, d 128: 260 us (1059 TFLOP/s; 266 with a single thread that runs the
+// issuing loop, whose descriptors then pass through general registers, 70 clocks an MMA).
 // With blocks of 128 keys, which leave TMEM for one S per tile, so that each tile's products and
 // softmax wait for one another, 280; with one tile at a time whose blocks the two softmax groups
 // share, as in attn_tc2.cuh, 320.  8 sequences of 1024 queries, 16 heads to a KV head, window
-// 2047: 549 us against 616 with blocks of 128 keys.
+// 2047: 538 us against 616 with blocks of 128 keys.
 // The clusters resident at once walk the tile list, cluster c taking tiles c, c + N, ...,
 // its two streams in turn; the last of an odd number both streams share by key blocks, and
 // stream 1's half reaches stream 0 through shared memory.
@@ -46,6 +47,7 @@
 // barriers, which every thread reaches on every path.
 #pragma once
 #include <cooperative_groups.h>
+#include <type_traits>
 #include "attn_tc2.cuh"
 #include "attn_window.cuh"
 
@@ -219,7 +221,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
   constexpr uint16_t kBoth = 0x3;
   // the streams take the cluster's units in turn, and share the blocks of the last of an odd number
   auto shared_unit = [&](int it) { return 2 * it + 1 == cl_units; };
-  auto unit_at = [&](int it) {
+  auto unit_of = [&](int it, int x) {
     const bool sh = shared_unit(it);
     WindowUnit u = window_unit(p, tab, cid + (2 * it + (sh ? 0 : x)) * ncl, ntp, span);
     const int mid = u.j0 + (u.j1 - u.j0 + 1) / 2;
@@ -227,6 +229,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
     if (sh && x == 1) u.j0 = mid;
     return u;
   };
+  auto unit_at = [&](int it) { return unit_of(it, x); };
   auto commit = [&](uint64_t* bar) {
     if constexpr (PAIR) ptx::tc_commit_pair(bar, kBoth);
     else ptx::tc_commit(bar);
@@ -346,8 +349,19 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
         }
       }
     }
-    if (rank == 0 && lane == 0) {
-      // ---------------- MMA issuer: one thread per stream (of CTA 0 for the pair) ----------------
+    // ---------------- MMA issuer: one warp per stream (of CTA 0 for the pair) ----------------
+    // The whole warp runs the loop and one elected lane issues: with everything uniform and the
+    // stream a constant the descriptors stay in uniform registers.
+    auto issue = [&](auto stream) {
+      constexpr int x = decltype(stream)::value;
+      uint8_t* sQ = smem + x * Cfg::STREAM;
+      uint8_t* sK = sQ + Cfg::Q_BYTES;
+      uint8_t* sV = sK + AWT_ST * Cfg::H_BYTES;
+      uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + 2 * Cfg::STREAM) + x * Cfg::BARS;
+      uint64_t *qpeer = qfull + 1, *qempty = qfull + 2, *pready = qfull + 3, *sfull = qfull + 5;
+      uint64_t *vempty = sfull + AWT_ST, *kfull = vempty + AWT_ST, *vfull = kfull + AWT_ST, *vpeer = vfull + AWT_ST;
+      const bool lead = ptx::elect_one();
+      auto commit_lead = [&](uint64_t* bar) { if (lead) commit(bar); };
       const uint32_t idesc_s = ptx::idesc_bf16(PAIR ? 256 : 128, AWT_BK, false);
       const uint32_t idesc_o = ptx::idesc_bf16(PAIR ? 256 : 128, D, true);
       const uint64_t q_d = ptx::sdesc_sw128(ptx::smem_u32(sQ), 16, 1024);
@@ -357,6 +371,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       const uint32_t k_lo = (uint32_t)k_d, k_hi = (uint32_t)(k_d >> 32);
       const uint32_t v_lo = (uint32_t)v_d, v_hi = (uint32_t)(v_d >> 32);
       const uint32_t s_t = tmem + (uint32_t)(x * 128), o_t = tmem + 256u + (uint32_t)(x * 128);
+      auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
       auto s_mmas = [&](int jj) {
         const uint32_t b0 = k_lo + (uint32_t)((jj % AWT_ST) * (Cfg::H_BYTES >> 4));
         const uint32_t s_b = s_t + (uint32_t)((jj & 1) * AWT_BK);
@@ -366,6 +381,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           for (int k = 0; k < 4; ++k) {
             const uint32_t a = q_lo + (uint32_t)(kb * 1024 + k * 2);
             const uint32_t bb = b0 + (uint32_t)(kb * 256 + k * 2);
+            if (!lead) continue;
             if constexpr (PAIR) ptx::mma_bf16_ss_pair(s_b, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
             else ptx::mma_bf16_ss_lh(s_b, a, q_hi, bb, k_hi, idesc_s, (kb | k) ? 1u : 0u);
           }
@@ -379,24 +395,25 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
       bool ok = true;
       int jg = 0, uq = 0;
       for (int it = 0; it < my_units && ok; ++it) {
-        const WindowUnit u = unit_at(it);
+        const WindowUnit u = unit_of(it, x);
         const int n = u.j1 - u.j0;
         if (n == 0) continue;
-        ok = ptx::mbar_wait_sleep(qfull, (uint32_t)uq & 1u);
-        if (PAIR && ok) ok = ptx::mbar_wait_cluster_sleep(qpeer, (uint32_t)uq & 1u);
+        ok = all(ptx::mbar_wait_sleep(qfull, (uint32_t)uq & 1u) &&
+                 (!PAIR || ptx::mbar_wait_cluster_sleep(qpeer, (uint32_t)uq & 1u)));
         for (int j = 0; j < min(n, 2) && ok; ++j) {
-          ok = k_landed(jg + j);
+          ok = all(k_landed(jg + j));
           if (!ok) break;
           ptx::tc_fence_after();
           s_mmas(jg + j);
-          commit(&sfull[(jg + j) % AWT_ST]);
+          commit_lead(&sfull[(jg + j) % AWT_ST]);
         }
         if (!ok) break;
-        if (n <= 2) commit(qempty);
+        if (n <= 2) commit_lead(qempty);
         // every wait of a block comes before its MMAs, which are issued back to back
         for (int j = 0; j < n && ok; ++j, ++jg) {
           const bool more = j + 2 < n;
-          ok = v_landed(jg) && (!more || k_landed(jg + 2)) && wait_pair(&pready[jg & 1], (uint32_t)(jg >> 1) & 1u);
+          ok = all(v_landed(jg) && (!more || k_landed(jg + 2)) &&
+                   wait_pair(&pready[jg & 1], (uint32_t)(jg >> 1) & 1u));
           if (!ok) break;
           ptx::tc_fence_after();
           // P: bf16 pairs in the first 32 columns of S
@@ -405,18 +422,23 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
           for (int k = 0; k < AWT_BK / 16; ++k) {
             const uint32_t a = s_t + (uint32_t)((jg & 1) * AWT_BK + k * 8);
             const uint32_t acc = (j > 0 || k > 0) ? 1u : 0u;
+            if (!lead) continue;
             if constexpr (PAIR) ptx::mma_bf16_ts_pair(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
             else ptx::mma_bf16_ts_lh(o_t, a, b0 + (uint32_t)(k * 128), v_hi, idesc_o, acc);
           }
-          commit(&vempty[jg % AWT_ST]);
+          commit_lead(&vempty[jg % AWT_ST]);
           if (more) {
             s_mmas(jg + 2);                // over P: after P.V has read it (issued in order)
-            commit(&sfull[(jg + 2) % AWT_ST]);
+            commit_lead(&sfull[(jg + 2) % AWT_ST]);
           }
-          if (j + 3 == n) commit(qempty);  // the unit's last S: its query buffer is free
+          if (j + 3 == n) commit_lead(qempty);  // the unit's last S: its query buffer is free
         }
         ++uq;
       }
+    };
+    if (rank == 0) {
+      if (warp == 2) issue(std::integral_constant<int, 0>{});
+      else issue(std::integral_constant<int, 1>{});
     }
   } else {
     // ---------------- softmax: one thread per row ----------------
