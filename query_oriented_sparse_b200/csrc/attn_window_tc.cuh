@@ -19,12 +19,13 @@
 // tile's start, end and masked blocks pass under the other's work.  S of block j + 2 is issued
 // behind P.V of block j, so a softmax warp finds the next S done while its last block's products
 // run.  A block then takes about 850 clocks per SM.  Measured on 4096 queries of 32 heads, 8 KV
-// heads, window 4096, d 128: 260 us (1059 TFLOP/s; 266 with a single thread that runs the
-// issuing loop, whose descriptors then pass through general registers, 70 clocks an MMA).
+// heads, window 4096, d 128: 247 us (1114 TFLOP/s; 260 without the cubic
+// exponentials below; 266 with one thread running the issuing loop, whose descriptors then pass
+// through general registers, 70 clocks an MMA).
 // With blocks of 128 keys, which leave TMEM for one S per tile, so that each tile's products and
 // softmax wait for one another, 280; with one tile at a time whose blocks the two softmax groups
 // share, as in attn_tc2.cuh, 320.  8 sequences of 1024 queries, 16 heads to a KV head, window
-// 2047: 538 us against 616 with blocks of 128 keys.
+// 2047: 522 us against 616 with blocks of 128 keys.
 // The clusters resident at once walk the tile list, cluster c taking tiles c, c + N, ...,
 // its two streams in turn; the last of an odd number both streams share by key blocks, and
 // stream 1's half reaches stream 0 through shared memory.
@@ -56,6 +57,7 @@ namespace quoka {
 constexpr int AWT_THREADS = 384;   // warps 0-1 load, 2-3 MMA, 4-7 and 8-11 softmax
 constexpr int AWT_ST = 4;          // K stages, and V stages, per stream
 constexpr int AWT_BK = 64;         // keys per block
+constexpr int AWT_FMA_EXP = 4;     // one of so many exponentials is taken on the FMA pipe (2: 259 us, 8: 256)
 
 template <int D>
 struct AwtCfg {
@@ -164,6 +166,21 @@ __device__ __forceinline__ void window_transpose4(uint4 (&v)[4], int lane) {
       if (up) v[i] = send; else v[i + o] = send;
     }
   }
+}
+
+// 2^t for t <= 16 on the FMA pipe: 2^round(t) from its exponent bits times a cubic in the rest
+// (|rest| <= 1/2; fitted for the least relative error, 7.5e-5 = 2^-13.7, a fiftieth of what the
+// rounding of P to bf16 may add).  Below 2^-126 it is zero; NaN stays NaN.
+__device__ __forceinline__ float2 window_exp2(float2 t) {
+  const float2 magic = make_float2(12583039.f, 12583039.f);      // 3 * 2^22 + 127: its low bits get n + 127
+  t = make_float2(ptx::max_nan(t.x, -127.f), ptx::max_nan(t.y, -127.f));
+  const float2 n = ptx::add2(t, magic);
+  const float2 r = ptx::add2(n, make_float2(-magic.x, -magic.y));
+  const float2 f = ptx::fma2(r, make_float2(-1.f, -1.f), t);
+  float2 q = ptx::fma2(f, make_float2(0.0551717746f, 0.0551717746f), make_float2(0.242611372f, 0.242611372f));
+  q = ptx::fma2(q, f, make_float2(0.693260970f, 0.693260970f));
+  q = ptx::fma2(q, f, make_float2(0.999928027f, 0.999928027f));
+  return ptx::mul2(q, make_float2(__int_as_float(__float_as_int(n.x) << 23), __int_as_float(__float_as_int(n.y) << 23)));
 }
 
 // The low n bits (n held to 0 .. 32).
@@ -524,7 +541,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 t = ptx::fma2(make_float2(s[c + 2 * i], s[c + 2 * i + 1]), scale2, minus_m2);
-            const float2 e = make_float2(ptx::ex2_approx(t.x), ptx::ex2_approx(t.y));
+            const float2 e = i % AWT_FMA_EXP == AWT_FMA_EXP - 1
+                                 ? window_exp2(t)
+                                 : make_float2(ptx::ex2_approx(t.x), ptx::ex2_approx(t.y));
             l2[i & 1] = ptx::add2(l2[i & 1], e);
             pk[i] = pack_bf16x2(e.x, e.y);
           }
