@@ -359,11 +359,13 @@ _HERE_AND_NOW = contextlib.nullcontext()
 def _on(dev: torch.device, stream: Optional[torch.cuda.Stream]):
     """Context of a call on tensors of `dev`: that device current, and `stream` (when given)
     the stream on which the call's outputs and scratch are allocated."""
+    if dev.type != "cuda":             # the kernels would follow host pointers
+        raise QuokaError(QUOKA_ERR_INVALID_ARG, f"the tensors are on {dev}, not on a CUDA device")
     if stream is not None:
         if stream.device != dev:
             raise QuokaError(QUOKA_ERR_INVALID_ARG, f"the stream is on {stream.device}, the tensors on {dev}")
         return torch.cuda.stream(stream)
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+    if dev.index != torch.cuda.current_device():
         return torch.cuda.device(dev)
     return _HERE_AND_NOW
 
