@@ -29,3 +29,36 @@ def test_host_tensors_are_refused(dtype):
         with pytest.raises(Bd.QuokaError, match="not on a CUDA device") as e:
             call()
         assert e.value.status == Bd.QUOKA_ERR_INVALID_ARG
+
+
+# ---- values that are not finite, all over the masked blocks ---------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+def test_bad_values_in_every_masked_block(d, cuda_device):
+    """Every seventh key holds NaN in one column of its own, so that each masked block of each tile
+    is cleaned, by lanes all over its warps and in both halves of the columns.  A row has NaN in
+    just the columns of the bad keys that it sees, and ten calls agree to the bit."""
+    prefix, window, n_sink, C, h_q, h_kv = (700, 0, 333), 150, 5, 500, 16, 4
+    g = torch.Generator().manual_seed(50)
+    off = [0]
+    for p in prefix:
+        off.append(off[-1] + p + C)
+    q = torch.randn(3, h_q, C, d, generator=g).to(BF)
+    k, v = torch.randn(h_kv, off[-1], d, generator=g).to(BF), torch.randn(h_kv, off[-1], d, generator=g).to(BF)
+    bad = torch.arange(0, off[-1], 7)
+    col = (37 * torch.arange(bad.numel())) % d
+    v[:, bad, col] = float("nan")
+    has = torch.zeros(off[-1], d, dtype=torch.bool)
+    has[bad, col] = True
+    args = q.cuda(), k.cuda(), v.cuda(), off, prefix, window, n_sink
+    first = Bd.window_chunk_attn(*args).cpu()
+    for b, P in enumerate(prefix):
+        j, at = torch.arange(P + C), torch.arange(P, P + C)[:, None]
+        seen = (j <= at) & ((j < n_sink) | (j > at - window))
+        want = (seen.float() @ has[off[b]:off[b] + P + C].float()) > 0
+        assert torch.equal(first[b].isnan(), want.expand(h_q, C, d))
+        assert not first[b].isinf().any()
+    for _ in range(10):
+        assert torch.equal(Bd.window_chunk_attn(*args).cpu().nan_to_num(77), first.nan_to_num(77))
+    assert Bd.device_error() == 0
