@@ -567,10 +567,17 @@ class PagedCache:
         self.block_table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=dev)
         self.seq_len = torch.zeros(batch, dtype=torch.int32, device=dev)
 
-    def _take(self, counts: Sequence[int]) -> List[List[int]]:
-        if sum(counts) > len(self.free):
-            raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{sum(counts)} pages needed, {len(self.free)} free")
-        return [[self.free.pop() for _ in range(n)] for n in counts]
+    def _pick(self, counts: Sequence[int]) -> List[List[int]]:
+        """The next free pages, counts[b] for each sequence.  They stay free until the call that
+        writes to them has been accepted (_taken): a refused call leaves the cache as it was."""
+        total = sum(counts)
+        if total > len(self.free):
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{total} pages needed, {len(self.free)} free")
+        last = iter(self.free[len(self.free) - total:][::-1])
+        return [[next(last) for _ in range(n)] for n in counts]
+
+    def _taken(self, pages: Sequence[Sequence[int]]) -> None:
+        del self.free[len(self.free) - sum(map(len, pages)):]
 
     def _table(self, pages: Sequence[Sequence[int]]) -> torch.Tensor:
         rows = [list(p) + [-1] * (self.max_pages - len(p)) for p in pages]
@@ -578,20 +585,24 @@ class PagedCache:
 
     def append(self, k_new: torch.Tensor, v_new: torch.Tensor, counts: Optional[Sequence[int]] = None) -> None:
         """Appends k_new / v_new [batch, h_kv, n, d], or the first counts[b] rows of each."""
-        n = int(k_new.shape[2])
+        n = _dims(k_new, "k_new", 4)[2]
         add = [n] * len(self.lens) if counts is None else [int(c) for c in counts]
         if len(add) != len(self.lens) or any(c < 0 or c > n for c in add):
             raise QuokaError(QUOKA_ERR_INVALID_ARG, "counts needs one entry in [0, n] per sequence")
         more = [-(-(l + c) // self.page_size) - len(p) for l, c, p in zip(self.lens, add, self.pages)]
         if any(len(p) + m > self.max_pages for p, m in zip(self.pages, more)):
             raise QuokaError(QUOKA_ERR_INVALID_ARG, "a sequence would need more than max_pages pages")
+        pages, table, new = self.pages, self.block_table, []
         if any(more):
-            self.pages = [p + m for p, m in zip(self.pages, self._take(more))]
-            self.block_table = self._table(self.pages)
+            new = self._pick(more)
+            pages = [p + m for p, m in zip(pages, new)]
+            table = self._table(pages)
         cnt = None if counts is None else torch.tensor(add, dtype=torch.int32).to(self.seq_len.device)
-        paged_append(k_new, v_new, self.k_pages, self.v_pages, self.block_table, self.seq_len, n_new=cnt,
+        paged_append(k_new, v_new, self.k_pages, self.v_pages, table, self.seq_len, n_new=cnt,
                      weight_pages=self.weight_pages)
-        self.seq_len = self.seq_len + (n if cnt is None else cnt)
+        seq_len = self.seq_len + (n if cnt is None else cnt)
+        self._taken(new)
+        self.pages, self.block_table, self.seq_len = pages, table, seq_len
         self.lens = [l + c for l, c in zip(self.lens, add)]
 
     def attend(self, q: torch.Tensor, window: Optional[int] = None, n_sink: int = 0) -> torch.Tensor:
@@ -608,12 +619,13 @@ class PagedCache:
         if len(want) != len(self.lens) or any(b < 0 for b in want):
             raise QuokaError(QUOKA_ERR_INVALID_ARG, "budget needs one entry >= 0 per sequence")
         keep = [min(l, b) for l, b in zip(self.lens, want)]
-        pages = self._take([-(-k // self.page_size) for k in keep])
+        pages = self._pick([-(-k // self.page_size) for k in keep])
         table = self._table(pages)
         dev = table.device
         idx, new_len = paged_evict(self.k_pages, self.v_pages, self.weight_pages, self.block_table, self.seq_len,
                                    max(max(self.lens), 1), torch.tensor(keep, dtype=torch.int32).to(dev),
                                    max(max(keep), 1), table, n_sink=n_sink, n_recent=n_recent)
+        self._taken(pages)
         for p in self.pages:
             self.free.extend(p)
         self.pages, self.block_table, self.seq_len, self.lens = pages, table, new_len, keep

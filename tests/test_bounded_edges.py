@@ -62,3 +62,57 @@ def test_bad_values_in_every_masked_block(d, cuda_device):
     for _ in range(10):
         assert torch.equal(Bd.window_chunk_attn(*args).cpu().nan_to_num(77), first.nan_to_num(77))
     assert Bd.device_error() == 0
+
+
+# ---- refused calls leave a paged cache as it was ----------------------------------------------------
+
+def _state(c):
+    return list(c.free), [list(p) for p in c.pages], list(c.lens), c.block_table.tolist(), c.seq_len.tolist()
+
+
+def _refused_calls(c, dev):
+    """Calls that pass the cache's own checks and are refused by the operator under it."""
+    rows = lambda n, dt=BF, d=64: torch.zeros(2, 2, n, d, dtype=dt, device=dev)    # noqa: E731
+    return [lambda: c.append(rows(40, F32), rows(40, F32)),                # another type
+            lambda: c.append(rows(40), rows(39)),                          # k and v differ
+            lambda: c.append(rows(40, d=128), rows(40, d=128)),
+            lambda: c.append(rows(40)[0], rows(40)[0]),                    # a dimension is missing
+            lambda: c.append(rows(40).transpose(2, 3).contiguous().transpose(2, 3), rows(40)),
+            lambda: c.append(rows(9000), rows(9000), [40, 40]),            # more rows than a call takes
+            lambda: c.evict(20, n_sink=-1),
+            lambda: c.evict([20, 3], n_recent=-1)]
+
+
+@pytest.mark.parametrize("i", range(8))
+def test_refused_calls_leave_the_cache_on_the_host(i):
+    """No GPU: the operators refuse every call, after the cache has looked for its pages."""
+    c = Bd.PagedCache(2, 4, 2, 64, BF, 20, 16, 10, "cpu", record=True)
+    c.pages, c.free, c.lens = [[0, 1], [2]], list(range(19, 2, -1)), [30, 5]
+    c.block_table, c.seq_len = c._table(c.pages), torch.tensor(c.lens, dtype=torch.int32)
+    was = _state(c)
+    for _ in range(3):
+        with pytest.raises(Bd.QuokaError):
+            _refused_calls(c, "cpu")[i]()
+        assert _state(c) == was
+
+
+@pytest.mark.gpu
+def test_refused_calls_leave_the_cache(cuda_device):
+    """The same on the GPU; afterwards every page can still be had, and one more is refused."""
+    c = Bd.PagedCache(2, 4, 2, 64, BF, 20, 16, 10, "cuda", record=True)
+    one = lambda n: torch.ones(2, 2, n, 64, dtype=BF, device="cuda")       # noqa: E731
+    c.append(one(30), one(30), [30, 5])
+    was = _state(c)
+    for call in _refused_calls(c, "cuda"):
+        with pytest.raises(Bd.QuokaError):
+            call()
+        assert _state(c) == was
+    c.append(one(130), one(130), [130, 123])
+    assert len(c.free) == 2 and c.lens == [160, 128]
+    was = _state(c)
+    with pytest.raises(Bd.QuokaError, match="max_pages"):
+        c.append(one(1), one(1))
+    assert _state(c) == was
+    c.evict(16)
+    assert len(c.free) == 18 and c.lens == [16, 16]
+    assert sorted(c.free + sum(c.pages, [])) == list(range(20)) and Bd.device_error() == 0
