@@ -438,7 +438,8 @@ quoka_status paged_append(const quoka_paged_shape* shape, const void* k_new, con
  * The query of head h (KV head g = h / G) of sequence b, n = seq_len[b], attends to the
  * keys { j < n : j < n_sink or j >= n - window } (the new token's own key, if it is to be
  * seen, has been appended: position n - 1), out = softmax(q . k^T / sqrt(head_dim)) . v
- * with fp32 accumulation and softmax, stored in `dtype`.  n = 0 gives zeros.
+ * with fp32 accumulation and softmax, stored in `dtype`.  n = 0 gives zeros; a row whose
+ * visible logits are all -infinity is 0 / 0, NaN (and so is what it adds to a record).
  * With a record, record[key] += sum over the G heads of the group of the key's softmax
  * weight, for every visible key of every (sequence, KV head); a page that several
  * sequences share receives all of their sums (in an order that is not fixed).

@@ -15,6 +15,11 @@
 // the logits are kept (fp32, base 2) and the record kernel adds each key's softmax weight,
 // summed over the group's heads, once the join has the row's maximum and sum.
 //
+// A sum of 0 stands for "no visible key" in partials, joins and results (such a row is zeros).  Keys
+// that are there but whose logits are all -infinity leave a maximum of -infinity and no weight
+// either, so their sum is set to 1: beside a finite maximum it weighs nothing, and alone it gives
+// the NaN of 0 / 0, as in the chunk kernels.
+//
 // This file: the split, the CUDA-core kernel (fp32), the join and the record kernel.  fp32 with
 // one head to a group reads at 5.8 TB/s (d 128, 16 sequences of 4K to 8K tokens); more heads
 // make it wait for the logits' shared-memory reads (4 heads: 3.7 TB/s).
@@ -167,6 +172,12 @@ __device__ __forceinline__ void stream_record_key(const StreamParams& p, const S
   if (row >= 0) atomicAdd(p.record + row, w);
 }
 
+// A row's output element from its sum of p v, maximum and sum: zero without a visible key, NaN where
+// every visible logit is -infinity.
+__device__ __forceinline__ float stream_result(float o, float M, float L) {
+  return L == 0.f ? 0.f : M == -INFINITY ? NAN : o / L;
+}
+
 template <typename T, int D, int R>
 constexpr int ast_smem_bytes(int batch) {
   return adc_smem_bytes<T, D, R>() + (2 * batch + 1) * 4;
@@ -214,6 +225,7 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 #pragma unroll
       for (int e = 0; e < EPL; ++e) acc[r][e] = 0.f;
     }
+    bool seen = false;                                     // a visible key so far
     for (int w = warp; w < sg.cnt * 4; w += NW) {          // 32-key batches of the segment
       const int j = sg.span.tile(sg.i0 + (w >> 2)) * AST_TILE + (w & 3) * 32 + lane;
       bool vis = sg.span.visible(j);
@@ -274,6 +286,7 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
           if (r < rows) lg[r] = sc[r];
       }
       if (!on) continue;
+      seen = true;
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         float mx = sc[r];
@@ -314,7 +327,7 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
 #pragma unroll
       for (int r = 0; r < R; ++r) {
         mls[(warp * R + r) * 2] = m[r];
-        mls[(warp * R + r) * 2 + 1] = l[r];
+        mls[(warp * R + r) * 2 + 1] = seen && l[r] == 0.f ? 1.f : l[r];
       }
     }
 #pragma unroll
@@ -334,13 +347,13 @@ attn_stream_kernel(const T* __restrict__ q, const T* __restrict__ k, const T* __
         const float* ww = reinterpret_cast<const float*>(smem + (R * D + NW * R * 2) * 4 +
                                                          w * (Cfg::STAGE + 32 * R * 4));
         if (lw != 0.f) {                                   // a warp without visible keys adds nothing
-          const float f = exp2f(mw - M);
+          const float f = M == -INFINITY ? 1.f : exp2f(mw - M);
           o = fmaf(ww[e], f, o);
           L = fmaf(lw, f, L);
         }
       }
       if (sg.whole) {
-        out[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + r0 + r) * D + d] = from_f32<T>(L == 0.f ? 0.f : o / L);
+        out[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + r0 + r) * D + d] = from_f32<T>(stream_result(o, M, L));
         if (d == 0 && p.logits) {
           p.unit_ml[((size_t)sg.unit * p.G + r0 + r) * 2] = M;
           p.unit_ml[((size_t)sg.unit * p.G + r0 + r) * 2 + 1] = L == 0.f ? 0.f : 1.f / L;

@@ -309,6 +309,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
       for (int r = 0; r < NR; ++r) { m[r] = -INFINITY; l[r] = 0.f; }
       bool started = false;                                 // O^T holds earlier tiles of the segment
+      uint32_t seen = 0;                                    // a box was loaded: the group's tiles had a visible key
       for (int i = 0; i < sg.cnt; ++i, ++n) {
         const int st = n % NST, buf = n & 1;
         if (!BYROW && buf != grp) continue;
@@ -327,7 +328,9 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
             for (int r = 0; r < 16; ++r) s[r0 + r] = __uint_as_float(w[r]);
           }
-          vis = sg.span.visible(j) && ((boxes[st] >> (kk / box)) & 1u);
+          const uint32_t there = boxes[st];
+          seen |= there;
+          vis = sg.span.visible(j) && ((there >> (kk / box)) & 1u);
           ptx::tmem_ld_wait();
         }
         bool up = false;
@@ -429,12 +432,17 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
       }
       ptx::named_bar(bar_g, 128);
       ptx::tc_fence_after();
+      // row r's sum (1 where visible keys weigh nothing: all their logits are -infinity)
+      auto row_sum = [&](int r) {
+        const float v = (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]);
+        return seen && v == 0.f ? 1.f : v;
+      };
       const int slot = 2 * c + (x == x0 ? 0 : 1);
       auto finish = [&](int r, float o, float M, float L) {  // row r_lo + r, dimension kk
         const int row = r_lo + r;
         if (sg.whole) {
           if (kk < D)
-            out[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + row) * D + kk] = __float2bfloat16_rn(L == 0.f ? 0.f : o / L);
+            out[((size_t)sg.b * p.h_q + (size_t)sg.g * p.G + row) * D + kk] = __float2bfloat16_rn(stream_result(o, M, L));
           if (kk == 0 && p.logits) {
             p.unit_ml[((size_t)sg.unit * p.G + row) * 2] = M;
             p.unit_ml[((size_t)sg.unit * p.G + row) * 2 + 1] = L == 0.f ? 0.f : 1.f / L;
@@ -458,8 +466,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
           for (int ri = 0; ri < 16; ++ri) {
             const int r = r0 + ri;
             if (r >= rows || !ok) break;
-            const float L = (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]);
-            finish(r, __uint_as_float(w[ri]), m[r], L);
+            finish(r, __uint_as_float(w[ri]), m[r], row_sum(r));
           }
         } else {
           // One group leaves its half of the segment's tiles, the other joins it to its own and
@@ -473,7 +480,7 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
               obuf[r * 128 + kk] = __uint_as_float(w[r]);
               if (kk == 0) {
                 ml[r] = m[r];
-                ml[N + r] = ok ? (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]) : 0.f;
+                ml[N + r] = ok ? row_sum(r) : 0.f;
               }
             }
           }
@@ -482,11 +489,12 @@ attn_stream_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_con
 #pragma unroll
             for (int r = 0; r < N; ++r) {
               if (r >= rows || !ok) break;
-              const float l0 = (wsum[r] + wsum[NR + r]) + (wsum[2 * NR + r] + wsum[3 * NR + r]), l1 = ml[N + r];
+              const float l0 = row_sum(r), l1 = ml[N + r];
               const float M = l1 != 0.f ? (l0 != 0.f ? fmaxf(m[r], ml[r]) : ml[r]) : m[r];
               // a group without visible keys has l = 0 and an O^T that may not be set
-              const float f0 = l0 != 0.f ? ptx::ex2_approx(m[r] - M) : 0.f;
-              const float f1 = l1 != 0.f ? ptx::ex2_approx(ml[r] - M) : 0.f;
+              const bool none = M == -INFINITY;              // (of both, then: factors of 1 keep their sums)
+              const float f0 = l0 == 0.f ? 0.f : none ? 1.f : ptx::ex2_approx(m[r] - M);
+              const float f1 = l1 == 0.f ? 0.f : none ? 1.f : ptx::ex2_approx(ml[r] - M);
               const float o = (l0 != 0.f ? __uint_as_float(w[r]) * f0 : 0.f) + (l1 != 0.f ? obuf[r * 128 + kk] * f1 : 0.f);
               finish(r, o, M, (l0 != 0.f ? l0 * f0 : 0.f) + (l1 != 0.f ? l1 * f1 : 0.f));
             }

@@ -4,6 +4,7 @@ the attention weights may be off by."""
 import pytest
 import torch
 
+import bounded_ref as R
 from query_oriented_sparse_b200 import binding as Bd
 
 BF, F32 = torch.bfloat16, torch.float32
@@ -116,3 +117,84 @@ def test_refused_calls_leave_the_cache(cuda_device):
     c.evict(16)
     assert len(c.free) == 18 and c.lens == [16, 16]
     assert sorted(c.free + sum(c.pages, [])) == list(range(20)) and Bd.device_error() == 0
+
+
+# ---- rows whose visible logits are all -infinity ----------------------------------------------------
+
+def _minus_inf(k, rows):
+    """Makes the logits of these rows of k [..., rows, d] -infinity for queries with q[..., 0] < 0."""
+    k[..., rows, :] = 0.0
+    k[..., rows, 0] = float("inf")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("h_q,h_kv,d", [(8, 2, 128), (4, 1, 64), (20, 1, 64), (48, 1, 128)])
+@pytest.mark.parametrize("C", [1, 3, 90])
+def test_window_rows_without_a_finite_logit(C, h_q, h_kv, d, dtype, cuda_device):
+    """Where a query sees such keys only, the softmax is 0 / 0: NaN, whatever the chunk's length.
+    Beside one finite logit they weigh nothing."""
+    g = torch.Generator().manual_seed(60)
+    for P, window, n_sink in ((300, 5, 0), (3000, 2500, 0), (3000, 2500, 2), (40, 1000, 0)):
+        n = P + C
+        q = torch.randn(1, h_q, C, d, generator=g).to(dtype)
+        q[..., 0] = -1.0
+        k, v = torch.randn(h_kv, n, d, generator=g).to(dtype), torch.randn(h_kv, n, d, generator=g).to(dtype)
+        _minus_inf(k, slice(n_sink, n))
+        out = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), (0, n), (P,), window, n_sink).cpu()
+        if n_sink == 0:
+            assert out.isnan().all(), (P, window)
+        else:                                       # what a cache of the first tokens alone gives
+            for h in range(h_q):
+                ks, vs = k[h * h_kv // h_q, :n_sink].double(), v[h * h_kv // h_q, :n_sink].double()
+                o, mag, _, S = R.attend(q[0, h].double(), ks, vs, torch.ones(C, n_sink, dtype=torch.bool))
+                R.assert_close(out[0, h], o, R.out_tol(o, mag, S, d, n_sink, dtype), f"head {h}")
+    assert Bd.device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("h_q,h_kv,d", [(8, 2, 128), (4, 1, 64), (20, 1, 64), (48, 1, 128)])
+@pytest.mark.parametrize("n", [1, 100, 700, 6000])
+def test_decode_rows_without_a_finite_logit(n, h_q, h_kv, d, dtype, cuda_device):
+    """Two sequences of such keys but for one key of the second, with and without a record; an
+    empty third one gives zeros.  CTAs that hold none but -infinity must not spoil the join."""
+    page = 16
+    per = -(-n // page)
+    g = torch.Generator().manual_seed(61)
+    q = torch.randn(3, h_q, 1, d, generator=g).to(dtype)
+    q[..., 0] = -1.0
+    k = torch.randn(2 * per, h_kv, page, d, generator=g).to(dtype)
+    v = torch.randn(2 * per, h_kv, page, d, generator=g).to(dtype)
+    at = (n // 3) // page, (n // 3) % page          # the second sequence's finite key
+    keep = k[per + at[0], :, at[1]].clone()
+    _minus_inf(k, slice(None))
+    k[per + at[0], :, at[1]] = keep
+    table = torch.arange(3 * per, dtype=torch.int32).view(3, per).clamp(max=2 * per - 1).cuda()
+    lens = torch.tensor([n, n, 0], dtype=torch.int32).cuda()
+    for record in (False, True):
+        w = torch.full((2 * per, h_kv, page), 5.0).cuda() if record else None
+        out = Bd.paged_decode_attn(q.cuda(), k.cuda(), v.cuda(), table, lens, n, weight_pages=w).cpu()
+        assert out[0].isnan().all() and not out[2].any()
+        want = v[per + at[0], :, at[1]].repeat_interleave(h_q // h_kv, 0)
+        assert torch.equal(out[1, :, 0], want)      # one weight of 1
+        if record:
+            w = w.cpu().transpose(0, 1).reshape(h_kv, 2, per * page)
+            assert w[:, 0, :n].isnan().all() and (w[:, :, n:] == 5.0).all()
+            ref = torch.full((n,), 5.0)
+            ref[n // 3] += h_q // h_kv
+            assert torch.equal(w[:, 1, :n], ref.expand(h_kv, n))
+    assert Bd.device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+def test_decode_with_bad_pages_alone_gives_zeros(dtype, cuda_device):
+    """Keys whose pages are not in the pools are not seen: a sequence without any other key."""
+    k, v = torch.randn(9, 2, 16, 64).to(dtype).cuda(), torch.randn(9, 2, 16, 64).to(dtype).cuda()
+    table = torch.tensor([[-1, 9, 100]], dtype=torch.int32).cuda()
+    w = torch.full((9, 2, 16), 5.0).cuda()
+    out = Bd.paged_decode_attn(torch.randn(1, 8, 1, 64).to(dtype).cuda(), k, v, table,
+                               torch.tensor([40], dtype=torch.int32).cuda(), 40, weight_pages=w)
+    assert Bd.device_error() == 4
+    assert not out.any() and (w == 5.0).all()
