@@ -19,9 +19,9 @@
 // tile's start, end and masked blocks pass under the other's work.  S of block j + 2 is issued
 // behind P.V of block j, so a softmax warp finds the next S done while its last block's products
 // run.  A block then takes about 850 clocks per SM.  Measured on 4096 queries of 32 heads, 8 KV
-// heads, window 4096, d 128: 247 us (1114 TFLOP/s; 260 without the cubic
-// exponentials below; 266 with one thread running the issuing loop, whose descriptors then pass
-// through general registers, 70 clocks an MMA).
+// heads, window 4096, d 128: 257 us (1085 TFLOP/s; 265 without the
+// exponentials on the FMA pipe below).  One thread running the issuing loop, whose descriptors then
+// pass through general registers, costs 6 us more (70 clocks an MMA).
 // With blocks of 128 keys, which leave TMEM for one S per tile, so that each tile's products and
 // softmax wait for one another, 280; with one tile at a time whose blocks the two softmax groups
 // share, as in attn_tc2.cuh, 320.  8 sequences of 1024 queries, 16 heads to a KV head, window
@@ -57,7 +57,7 @@ namespace quoka {
 constexpr int AWT_THREADS = 384;   // warps 0-1 load, 2-3 MMA, 4-7 and 8-11 softmax
 constexpr int AWT_ST = 4;          // K stages, and V stages, per stream
 constexpr int AWT_BK = 64;         // keys per block
-constexpr int AWT_FMA_EXP = 4;     // one of so many exponentials is taken on the FMA pipe (2: 259 us, 8: 256)
+constexpr int AWT_FMA_EXP = 4;     // one of so many exponentials is taken on the FMA pipe: 257 us (3: 258, 5: 263, 8: 262, none 265)
 
 template <int D>
 struct AwtCfg {
@@ -178,18 +178,21 @@ __device__ __forceinline__ void window_transpose4(uint4 (&v)[4], int lane) {
   }
 }
 
-// 2^t for t <= 16 on the FMA pipe: 2^round(t) from its exponent bits times a cubic in the rest
-// (|rest| <= 1/2; fitted for the least relative error, 7.5e-5 = 2^-13.7, a fiftieth of what the
-// rounding of P to bf16 may add).  Below 2^-126 it is zero; NaN stays NaN.
+// 2^t for t <= 16 on the FMA pipe: 2^round(t) from its exponent bits times a polynomial of degree 5
+// in the rest (|rest| <= 1/2; fitted for the least relative error by Remez exchange: 7.5e-8, in
+// fp32 2.2e-7 = 2^-22.1, which is what ex2.approx may be off by too, so that a weight does not
+// depend on its key's place in the block).  Below 2^-126 it is zero; NaN stays NaN.
 __device__ __forceinline__ float2 window_exp2(float2 t) {
   const float2 magic = make_float2(12583039.f, 12583039.f);      // 3 * 2^22 + 127: its low bits get n + 127
   t = make_float2(ptx::max_nan(t.x, -127.f), ptx::max_nan(t.y, -127.f));
   const float2 n = ptx::add2(t, magic);
   const float2 r = ptx::add2(n, make_float2(-magic.x, -magic.y));
   const float2 f = ptx::fma2(r, make_float2(-1.f, -1.f), t);
-  float2 q = ptx::fma2(f, make_float2(0.0551717746f, 0.0551717746f), make_float2(0.242611372f, 0.242611372f));
-  q = ptx::fma2(q, f, make_float2(0.693260970f, 0.693260970f));
-  q = ptx::fma2(q, f, make_float2(0.999928027f, 0.999928027f));
+  float2 q = ptx::fma2(f, make_float2(1.32764725e-3f, 1.32764725e-3f), make_float2(9.67554096e-3f, 9.67554096e-3f));
+  q = ptx::fma2(q, f, make_float2(0.0555071309f, 0.0555071309f));
+  q = ptx::fma2(q, f, make_float2(0.240221202f, 0.240221202f));
+  q = ptx::fma2(q, f, make_float2(0.693146944f, 0.693146944f));
+  q = ptx::fma2(q, f, make_float2(1.00000012f, 1.00000012f));
   return ptx::mul2(q, make_float2(__int_as_float(__float_as_int(n.x) << 23), __int_as_float(__float_as_int(n.y) << 23)));
 }
 

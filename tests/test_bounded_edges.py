@@ -198,3 +198,42 @@ def test_decode_with_bad_pages_alone_gives_zeros(dtype, cuda_device):
                                torch.tensor([40], dtype=torch.int32).cuda(), 40, weight_pages=w)
     assert Bd.device_error() == 4
     assert not out.any() and (w == 5.0).all()
+
+
+# ---- what a weight may be off by --------------------------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("place", range(8))
+def test_weights_are_fp32_wherever_their_key_lies(place, d, cuda_device):
+    """bf16 chunks: the sum of the weights, read off the result.
+
+    Key 0 has logit 0, value 1 and weight 1, rounded to bf16 without an error; the keys at
+    `place` (mod 8) have a logit x in [-5, 0] of each row's own and value 0, every other key a
+    logit far below.  So the result is 1 / (1 + M e^x) in bf16.  x is exact in fp32 up to the
+    scaling.  Relative errors before the last rounding: the exponent |x log2 e| <= 7.3 is off by
+    4 2^-24 of itself (scale, its division and square root, one rounding), 7.3 ln 2 2^-22 < 2^-19.6
+    of the weight; the exponential 2^-22; the sum (16 terms to an accumulator, 8 blocks, joins: 30
+    roundings) 30 2^-24 < 2^-19; 1 / l and its product 2^-23: in all less than 2^-18.  The result
+    is a rounding to bf16 of something in between, and rounding is monotone."""
+    h_q, h_kv, C, P = 32, 2, 256, 448
+    g = torch.Generator().manual_seed(70 + place)
+    q = torch.zeros(1, h_q, C, d)
+    q[..., 0] = -4 * torch.rand(1, h_q, C, generator=g)
+    q[..., 1] = 1.0
+    q[..., 2] = -torch.rand(1, h_q, C, generator=g)
+    q = q.to(BF)
+    k, v = torch.zeros(h_kv, P + C, d), torch.zeros(h_kv, P + C, d)
+    k[:, 1:, 1] = -4096.0
+    rows = torch.arange(place, P, 8)
+    rows = rows[rows > 0]
+    unit = 8.0 if d == 64 else 11.0
+    k[:, rows, 0], k[:, rows, 1], k[:, rows, 2] = unit, 0.0, unit / 256
+    k[:, 0], v[:, 0] = 0.0, 1.0
+    out = Bd.window_chunk_attn(q.cuda(), k.to(BF).cuda(), v.to(BF).cuda(), (0, P + C), (P,), P + C, 0).cpu()
+    x = (q[..., 0].double() * unit + q[..., 2].double() * (unit / 256)) / d ** 0.5
+    ref = 1 / (1 + rows.numel() * torch.exp(x))[..., None]
+    lo, hi = (ref * (1 - 2.0 ** -18)).to(BF), (ref * (1 + 2.0 ** -18)).to(BF)
+    off = ~((lo <= out) & (out <= hi))
+    assert not off.any(), f"{int(off.any(-1).sum())} of {h_q * C} rows"
+    assert Bd.device_error() == 0
