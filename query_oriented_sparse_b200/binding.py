@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libquoka.so")
 
 QUOKA_OK, QUOKA_ERR_INVALID_ARG, QUOKA_ERR_UNSUPPORTED, QUOKA_ERR_WORKSPACE, QUOKA_ERR_CUDA = range(5)
 QUOKA_F32, QUOKA_BF16 = 0, 1
+QUOKA_MAX_EVICT_LEN = 786432
 STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE", 4: "CUDA"}
 
 # (name, restype, argtypes) of every symbol include/quoka.h declares
@@ -612,14 +613,20 @@ class PagedCache:
                                  weight_pages=self.weight_pages)
 
     def evict(self, budget: Union[int, Sequence[int]], n_sink: int = 0, n_recent: int = 0) -> torch.Tensor:
-        """Shrinks every sequence to its budget; returns the kept positions of each KV head."""
+        """Shrinks every sequence to its budget; returns the kept positions of each KV head.  The
+        records that it goes by are what attend() has added since a row was appended.  The kept rows
+        go to free pages where those suffice for all sequences, else (a cache that is full) each
+        sequence's go through a copy of its pages back into the first of them."""
         if self.weight_pages is None:
             raise QuokaError(QUOKA_ERR_INVALID_ARG, "this cache keeps no weight record")
         want = [int(budget)] * len(self.lens) if isinstance(budget, int) else [int(b) for b in budget]
         if len(want) != len(self.lens) or any(b < 0 for b in want):
             raise QuokaError(QUOKA_ERR_INVALID_ARG, "budget needs one entry >= 0 per sequence")
         keep = [min(l, b) for l, b in zip(self.lens, want)]
-        pages = self._pick([-(-k // self.page_size) for k in keep])
+        need = [-(-k // self.page_size) for k in keep]
+        if sum(need) > len(self.free):
+            return self._evict_in_turn(keep, need, n_sink, n_recent)
+        pages = self._pick(need)
         table = self._table(pages)
         dev = table.device
         idx, new_len = paged_evict(self.k_pages, self.v_pages, self.weight_pages, self.block_table, self.seq_len,
@@ -629,6 +636,38 @@ class PagedCache:
         for p in self.pages:
             self.free.extend(p)
         self.pages, self.block_table, self.seq_len, self.lens = pages, table, new_len, keep
+        return idx
+
+    def _evict_in_turn(self, keep: Sequence[int], need: Sequence[int], n_sink: int, n_recent: int) -> torch.Tensor:
+        """evict() without free pages, one sequence at a time (a sequence that keeps all of its rows
+        stays as it is).  The books follow each sequence, should a later copy find no memory."""
+        # what paged_evict would refuse, before the first sequence changes
+        if n_sink < 0 or n_recent < 0:
+            raise QuokaError(QUOKA_ERR_INVALID_ARG, f"n_sink={n_sink} and n_recent={n_recent} must be >= 0")
+        if max(self.lens) > QUOKA_MAX_EVICT_LEN:
+            raise QuokaError(QUOKA_ERR_UNSUPPORTED, f"length {max(self.lens)} exceeds {QUOKA_MAX_EVICT_LEN}")
+        pools, dev = (self.k_pages, self.v_pages, self.weight_pages), self.k_pages.device
+        budget = torch.tensor(keep, dtype=torch.int32).to(dev)
+        idx = torch.full((len(keep), pools[0].shape[1], max(max(keep), 1)), -1, dtype=torch.int32, device=dev)
+        self.block_table, self.seq_len = self.block_table.clone(), self.seq_len.clone()
+        self.pages, self.lens = list(self.pages), list(self.lens)
+        for b, (k, m) in enumerate(zip(keep, need)):
+            n, old = self.lens[b], self.pages[b]
+            if k == n:
+                idx[b, :, :n] = torch.arange(n, dtype=torch.int32, device=dev)
+                continue
+            if k > 0:
+                at = torch.tensor(old).to(dev)
+                copies = [torch.cat([p[at], p.new_zeros(m, *p.shape[1:])]) for p in pools]
+                table = torch.arange(len(old) + m, dtype=torch.int32, device=dev)[None]
+                idx[b, :, :k] = paged_evict(*copies, table[:, :len(old)], self.seq_len[b:b + 1], n, budget[b:b + 1], k,
+                                            table[:, len(old):], n_sink=n_sink, n_recent=n_recent)[0]
+                for p, c in zip(pools, copies):
+                    p[at[:m]] = c[len(old):]
+            self.block_table[b, m:] = -1
+            self.seq_len[b:b + 1] = budget[b:b + 1]
+            self.pages[b], self.lens[b] = old[:m], k
+            self.free.extend(old[m:])
         return idx
 
 

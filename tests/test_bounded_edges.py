@@ -1,6 +1,8 @@
 """Edges of the window and paged-cache calls: tensors that are not on a GPU, calls that are
 refused half way, caches without a free page, rows whose softmax has no finite logit, and what
 the attention weights may be off by."""
+import os
+
 import pytest
 import torch
 
@@ -236,4 +238,71 @@ def test_weights_are_fp32_wherever_their_key_lies(place, d, cuda_device):
     lo, hi = (ref * (1 - 2.0 ** -18)).to(BF), (ref * (1 + 2.0 ** -18)).to(BF)
     off = ~((lo <= out) & (out <= hi))
     assert not off.any(), f"{int(off.any(-1).sum())} of {h_q * C} rows"
+    assert Bd.device_error() == 0
+
+
+# ---- eviction from a cache without free pages ---------------------------------------------------------
+
+def test_eviction_limit_is_the_headers():
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "quoka.h")
+    assert f"#define QUOKA_MAX_EVICT_LEN {Bd.QUOKA_MAX_EVICT_LEN}\n" in open(path).read()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("spare", [0, 2])
+@pytest.mark.parametrize("lens,budget,n_sink,n_recent", [
+    ((64, 40, 16, 100), [20, 40, 0, 17], 2, 5),      # one keeps everything, one nothing
+    ((64, 40, 16, 100), [63, 39, 15, 99], 0, 0),     # as many pages as before
+    ((700, 1, 0, 33), [333, 5, 7, 32], 40, 300),
+])
+def test_a_full_cache_is_evicted(lens, budget, n_sink, n_recent, spare, dtype, cuda_device):
+    """Fewer free pages than the kept rows need: the same rows are kept as with free pages, the
+    pages are given back, and the cache can be used on."""
+    B, h_q, h_kv, d, page = len(lens), 8, 2, 128, 16
+    g = torch.Generator().manual_seed(80)
+    used = sum(-(-n // page) for n in lens)
+    kn, vn = (torch.randn(B, h_kv, max(lens), d, generator=g).to(dtype) for _ in range(2))
+
+    def filled(num_pages):
+        c = Bd.PagedCache(B, h_q, h_kv, d, dtype, num_pages, page, 50, "cuda", record=True)
+        c.append(kn.cuda(), vn.cuda(), lens)
+        c.weight_pages.copy_(0)
+        for b, n in enumerate(lens):
+            w = torch.rand(h_kv, n, generator=torch.Generator().manual_seed(81 + b))
+            j = torch.arange(n)
+            c.weight_pages[c.block_table[b].cpu()[j // page].long().cuda(), :, (j % page).cuda()] = w.T.cuda()
+        return c
+
+    def rows(c):
+        return [[R.gather_pages(t.cpu(), c.block_table[b].cpu(), n) if n else None for b, n in enumerate(c.lens)]
+                for t in (c.k_pages, c.v_pages, c.weight_pages)]
+
+    full, roomy = filled(used + spare), filled(4 * used)
+    assert len(full.free) == spare < sum(-(-min(n, b) // page) for n, b in zip(lens, budget))
+    was = _state(full)
+    for bad in (dict(n_sink=-1), dict(n_recent=-1)):
+        with pytest.raises(Bd.QuokaError) as e:
+            full.evict(budget, **bad)
+        assert e.value.status == Bd.QUOKA_ERR_INVALID_ARG and _state(full) == was
+    before = rows(full)
+    idx = full.evict(budget, n_sink=n_sink, n_recent=n_recent)
+    assert torch.equal(idx, roomy.evict(budget, n_sink=n_sink, n_recent=n_recent))
+    keep = [min(n, b) for n, b in zip(lens, budget)]
+    for b, k in enumerate(keep):
+        for h in range(h_kv):
+            want = R.evict_rows(before[2][b][h], lens[b], budget[b], n_sink, n_recent) if lens[b] else []
+            assert idx[b, h].tolist() == want + [-1] * (idx.shape[2] - k)
+            for t, old in zip(rows(full), before):
+                if k:
+                    assert torch.equal(t[b][h], old[b][h][want])
+    assert full.lens == keep and full.seq_len.tolist() == keep
+    assert [len(p) for p in full.pages] == [-(-k // page) for k in keep]
+    assert sorted(full.free + sum(full.pages, [])) == list(range(used + spare))
+    assert full.block_table.tolist() == full._table(full.pages).tolist()
+    q, new = torch.randn(B, h_q, 1, d, generator=g).to(dtype).cuda(), kn[:, :, :1].contiguous().cuda()
+    counts = [1 if k % page else 0 for k in keep]    # (the second case leaves no page free)
+    for c in (full, roomy):
+        c.append(new, new, counts)
+    assert torch.equal(full.attend(q), roomy.attend(q))
     assert Bd.device_error() == 0
