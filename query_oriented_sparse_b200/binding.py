@@ -383,6 +383,12 @@ def _need(name: str, t: torch.Tensor, shape: Tuple[int, ...], dtype: torch.dtype
     raise QuokaError(QUOKA_ERR_INVALID_ARG, f"{name} must be contiguous")
 
 
+def _c_int(x: int) -> int:
+    """x held to what a C int holds (ctypes would keep its low 32 bits: a window of 2^32 + 5 keys
+    would be one of 5)."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def _adr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
@@ -405,7 +411,7 @@ def _dims(t: torch.Tensor, name: str, n: int) -> Tuple[int, ...]:
 
 
 def window_workspace_size(shape: QuokaShape, max_prefix: int, window: int) -> int:
-    return int(lib().window_chunk_attn_workspace_size(ctypes.byref(shape), int(max_prefix), int(window)))
+    return int(lib().window_chunk_attn_workspace_size(ctypes.byref(shape), _c_int(max_prefix), _c_int(window)))
 
 
 def window_chunk_attn(q_chunk: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -434,7 +440,7 @@ def window_chunk_attn(q_chunk: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
         workspace, ws_bytes = _scratch(workspace, n, dev)
         _check(lib().window_chunk_attn(
             ctypes.byref(shape), _adr(q_chunk), _adr(k_cache), _adr(v_cache), _host_i64(kv_off),
-            _host_i32(prefix_len), int(window), int(n_sink), _adr(out), _adr(workspace), ws_bytes,
+            _host_i32(prefix_len), _c_int(window), _c_int(n_sink), _adr(out), _adr(workspace), ws_bytes,
             _stream(stream)))
     return out
 
@@ -485,7 +491,7 @@ def paged_append(k_new: torch.Tensor, v_new: torch.Tensor, k_pages: torch.Tensor
 
 
 def paged_decode_workspace_size(shape: QuokaPagedShape, max_len: int, with_record: bool) -> int:
-    return int(lib().paged_decode_attn_workspace_size(ctypes.byref(shape), int(max_len), int(with_record)))
+    return int(lib().paged_decode_attn_workspace_size(ctypes.byref(shape), _c_int(max_len), int(with_record)))
 
 
 def paged_decode_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -514,7 +520,7 @@ def paged_decode_attn(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Ten
             if workspace is None else 0, dev)
         _check(lib().paged_decode_attn(
             ctypes.byref(shape), _adr(q), _adr(k_pages), _adr(v_pages), _adr(block_table), _adr(seq_len),
-            int(max_len), int(max_len if window is None else window), int(n_sink), _adr(weight_pages),
+            _c_int(max_len), _c_int(max_len if window is None else window), _c_int(n_sink), _adr(weight_pages),
             _adr(out), _adr(workspace), ws_bytes, _stream(stream)))
     return out
 
@@ -545,7 +551,7 @@ def paged_evict(k_pages: torch.Tensor, v_pages: torch.Tensor, weight_pages: torc
             _need("new_len", new_len, (shape.batch,), torch.int32, dev)
         _check(lib().paged_evict(
             ctypes.byref(shape), _adr(k_pages), _adr(v_pages), _adr(weight_pages), _adr(block_table),
-            _adr(seq_len), int(max_len), _adr(budget), int(b_max), int(n_sink), int(n_recent),
+            _adr(seq_len), _c_int(max_len), _adr(budget), _c_int(b_max), _c_int(n_sink), _c_int(n_recent),
             _adr(dst_table), dst_pages, _adr(idx_out), _adr(new_len), _stream(stream)))
     return idx_out, new_len
 

@@ -306,3 +306,41 @@ def test_a_full_cache_is_evicted(lens, budget, n_sink, n_recent, spare, dtype, c
         c.append(new, new, counts)
     assert torch.equal(full.attend(q), roomy.attend(q))
     assert Bd.device_error() == 0
+
+
+# ---- counts past 32 bits --------------------------------------------------------------------------------
+
+def test_sizes_past_32_bits_on_the_host():
+    shape = Bd.make_shape(1, 8, 2, 128, 16, BF)
+    most = Bd.window_workspace_size(shape, 5000, 2 ** 31 - 1)
+    assert most > 0 and Bd.window_workspace_size(shape, 5000, 2 ** 32 + 10) == most
+    assert Bd.window_workspace_size(shape, 5000, -2 ** 32 + 10) == 0
+    pages = Bd.QuokaPagedShape(2, 8, 2, 128, Bd.QUOKA_BF16, 16, 100, 10)
+    assert Bd.paged_decode_workspace_size(pages, 2 ** 32 + 160, False) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("C", [1, 20])
+def test_counts_past_32_bits(C, cuda_device):
+    """A window or a number of first tokens of more than 2^31 keys is all of them, not its low
+    32 bits; a length or budget of that size is refused."""
+    g = torch.Generator().manual_seed(90)
+    P, n = 300, 300 + C
+    q = torch.randn(1, 8, C, 64, generator=g).to(BF).cuda()
+    k, v = (torch.randn(2, n, 64, generator=g).to(BF).cuda() for _ in range(2))
+    want = Bd.window_chunk_attn(q, k, v, (0, n), (P,), n)
+    assert torch.equal(Bd.window_chunk_attn(q, k, v, (0, n), (P,), 2 ** 32 + 5), want)
+    assert torch.equal(Bd.window_chunk_attn(q, k, v, (0, n), (P,), 3, n_sink=2 ** 32), want)
+    c = Bd.PagedCache(1, 8, 2, 64, BF, 64, 16, 30, "cuda", record=True)
+    c.append(k[None].contiguous(), v[None].contiguous())
+    qt = q[:, :, -1:].contiguous()
+    want = c.attend(qt)
+    assert torch.equal(c.attend(qt, window=2 ** 32 + 5), want)
+    assert torch.equal(c.attend(qt, window=3, n_sink=2 ** 32 + 1), want)
+    args = c.k_pages, c.v_pages
+    with pytest.raises(Bd.QuokaError):
+        Bd.paged_decode_attn(qt, *args, c.block_table, c.seq_len, 2 ** 32 + n)
+    with pytest.raises(Bd.QuokaError):
+        Bd.paged_evict(*args, c.weight_pages, c.block_table, c.seq_len, n, c.seq_len, 8, c.block_table.clone(), n_sink=-2 ** 32)
+    idx = c.evict(20, n_recent=2 ** 32 + 1)
+    assert idx[0, 0].tolist() == list(range(n - 20, n)) and Bd.device_error() == 0
