@@ -344,3 +344,78 @@ def test_counts_past_32_bits(C, cuda_device):
         Bd.paged_evict(*args, c.weight_pages, c.block_table, c.seq_len, n, c.seq_len, 8, c.block_table.clone(), n_sink=-2 ** 32)
     idx = c.evict(20, n_recent=2 ** 32 + 1)
     assert idx[0, 0].tolist() == list(range(n - 20, n)) and Bd.device_error() == 0
+
+
+# ---- what the weight record must leave alone ------------------------------------------------------------
+
+UNUSED = 77.0
+
+
+def _recorded(dtype, h_q, h_kv, d, page, lens, table_of=None, window=None, n_sink=0):
+    """Attention over pools whose record holds UNUSED in every slot without a key: the record
+    before and after, [page, head, slot], on the CPU, and the 64-bit weights per sequence."""
+    g = torch.Generator().manual_seed(100)
+    per = [-(-n // page) for n in lens]
+    N = sum(per) + 4
+    perm = torch.randperm(N, generator=g).tolist()
+    table = torch.full((len(lens), max(max(per), 1)), -1, dtype=torch.int32)
+    was = torch.full((N, h_kv, page), UNUSED)
+    for b, (n, m) in enumerate(zip(lens, per)):
+        pages = [perm.pop() for _ in range(m)]
+        table[b, :m] = torch.tensor(pages, dtype=torch.int32)
+        j = torch.arange(n)
+        was[table[b][j // page].long(), :, j % page] = torch.rand(n, h_kv, generator=g)
+    k, v = torch.randn(N, h_kv, page, d, generator=g).to(dtype), torch.randn(N, h_kv, page, d, generator=g).to(dtype)
+    q = torch.randn(len(lens), h_q, 1, d, generator=g).to(dtype)
+    given = table if table_of is None else table_of(table.clone())
+    w = was.cuda()
+    Bd.paged_decode_attn(q.cuda(), k.cuda(), v.cuda(), given.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                         max(max(lens), 1), window=window, n_sink=n_sink, weight_pages=w)
+    want, tol = was.double(), torch.zeros(was.shape, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        j = torch.arange(n)
+        there = (given[b][j // page] >= 0) & (given[b][j // page] < N)
+        seen = there & ((j < n_sink) | (j >= n - (window or n)))
+        if not seen.any():
+            continue
+        j = j[seen]
+        for h in range(h_kv):
+            kk = k[table[b][j // page].long(), h, j % page].double()
+            G = h_q // h_kv
+            _, _, p, S = R.attend(q[b, h * G:(h + 1) * G, 0].double(), kk, kk, torch.ones(G, j.numel(), dtype=torch.bool))
+            at = table[b][j // page].long(), h, j % page
+            want[at] += p.sum(0)
+            # each head's weight, the sum over the heads, and the addition in memory
+            tol[at] = (p * R.weight_err(d, j.numel(), S)).sum(0) + G * 2.0 ** -24 * p.sum(0) + want[at] * 2.0 ** -24
+    return was, w.cpu(), want, tol
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("h_q,h_kv,d", [(8, 2, 128), (4, 1, 64), (5, 1, 128), (20, 1, 64), (64, 1, 128)])
+@pytest.mark.parametrize("page,lens,window,n_sink", [
+    (8, (1, 7, 0, 300), None, 0), (16, (2000, 5, 131), None, 0), (24, (700, 9), 100, 5),
+    (256, (257, 255, 256), None, 0), (16, (9000,), 3000, 40), (16, tuple(range(1, 200, 3)), 50, 1)])
+def test_record_changes_visible_keys_only(page, lens, window, n_sink, h_q, h_kv, d, dtype, cuda_device):
+    was, w, want, tol = _recorded(dtype, h_q, h_kv, d, page, lens, window=window, n_sink=n_sink)
+    assert Bd.device_error() == 0
+    assert torch.equal(w[tol == 0], was[tol == 0])          # to the bit: unseen, unused and spare slots
+    R.assert_close(w, want, tol, "record")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("value", [-1, 1 << 30, "pages"])
+@pytest.mark.parametrize("lens", [(200, 90), (6000, 90)])
+def test_record_beside_a_bad_page(lens, value, dtype, cuda_device):
+    """The keys of a page that is not in the pools take no weight and get none; everybody else's
+    weights are what they are without those keys."""
+    def table_of(t):
+        t[0, 3] = sum(-(-n // 16) for n in lens) + 4 if value == "pages" else value
+        return t
+
+    was, w, want, tol = _recorded(dtype, 8, 2, 128, 16, lens, table_of)
+    assert Bd.device_error() == 4
+    assert torch.equal(w[tol == 0], was[tol == 0])
+    R.assert_close(w, want, tol, "record")
+    assert int((tol[:, 0] != 0).sum()) == sum(lens) - 16
