@@ -419,3 +419,33 @@ def test_record_beside_a_bad_page(lens, value, dtype, cuda_device):
     assert torch.equal(w[tol == 0], was[tol == 0])
     R.assert_close(w, want, tol, "record")
     assert int((tol[:, 0] != 0).sum()) == sum(lens) - 16
+
+
+# ---- chunks that see more first tokens than latest ones ---------------------------------------------------
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [F32, BF], ids=["f32", "bf16"])
+@pytest.mark.parametrize("h_q,h_kv,d,C,prefix,window,n_sink,split", [
+    (32, 8, 128, 2, (3000,), 64, 2000, False),       # whole tiles: the window alone is short
+    (8, 2, 64, 2, (3000, 1500), 64, 2000, False),
+    (8, 2, 128, 9, (5000,), 1100, 3333, True),        # units of first tokens only, of both, of the window only
+    (8, 2, 64, 9, (5000, 3500), 1100, 2000, True),
+    (4, 4, 128, 40, (4000,), 1200, 2701, True),
+])
+def test_mostly_first_tokens(h_q, h_kv, d, C, prefix, window, n_sink, split, dtype, cuda_device):
+    shape = Bd.make_shape(len(prefix), h_q, h_kv, d, C, dtype)
+    assert (Bd.window_workspace_size(shape, max(prefix), window) > 0) == split
+    g = torch.Generator().manual_seed(110)
+    off = [0]
+    for p in prefix:
+        off.append(off[-1] + p + C)
+    q = torch.randn(len(prefix), h_q, C, d, generator=g).to(dtype)
+    k, v = (torch.randn(h_kv, off[-1], d, generator=g).to(dtype) for _ in range(2))
+    out = Bd.window_chunk_attn(q.cuda(), k.cuda(), v.cuda(), off, prefix, window, n_sink).cpu()
+    assert Bd.device_error() == 0
+    for b, P in enumerate(prefix):
+        seen = R.window_seen(P, C, P + C, window, n_sink)
+        for h in range(h_q):
+            ks, vs = (t[h * h_kv // h_q, off[b]:off[b + 1]].double() for t in (k, v))
+            o, mag, _, S = R.attend(q[b, h].double(), ks, vs, seen)
+            R.assert_close(out[b, h], o, R.out_tol(o, mag, S, d, seen.sum(-1, keepdim=True), dtype), f"{b} {h}")
