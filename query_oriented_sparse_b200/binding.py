@@ -386,7 +386,8 @@ def _need(name: str, t: torch.Tensor, shape: Tuple[int, ...], dtype: torch.dtype
 def _c_int(x: int) -> int:
     """x held to what a C int holds (ctypes would keep its low 32 bits: a window of 2^32 + 5 keys
     would be one of 5)."""
-    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+    x = int(x)
+    return x if -2 ** 31 <= x < 2 ** 31 else 2 ** 31 - 1 if x > 0 else -2 ** 31
 
 
 def _adr(t: Optional[torch.Tensor]):
