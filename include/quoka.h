@@ -361,9 +361,11 @@ quoka_status sparse_chunk_attn_selcache(const quoka_shape* shape, const void* q_
  * P = prefix_len[b], attends to the keys
  *     { j <= p : j < n_sink  or  j > p - window }
  * of its sequence, out = softmax(q . k^T / sqrt(head_dim)) . v with fp32 accumulation and
- * softmax, stored in `dtype`.  window >= P + chunk sees every earlier key.  Each query sees
- * at least its own key.  Rows of the cache that no query sees are not used, and what a key
- * or value holds reaches only the queries that see it, infinities and NaN included.
+ * softmax, stored in `dtype` (bf16: the weights are rounded to bf16 for their product with v,
+ * once their sum has been taken).  window >= P + chunk sees every earlier key.  Each query sees
+ * at least its own key; one whose visible logits are all -infinity gets 0 / 0, NaN.  Rows of the
+ * cache that no query sees are not used, and what a key or value holds reaches only the queries
+ * that see it, infinities and NaN included.
  * chunk = 1 (a decode step) runs the kernel of paged_decode_attn, the keys of each
  * (sequence, KV head) split over the SMs; longer chunks run per query tile, whose keys are
  * split when the tiles are few.
@@ -438,7 +440,8 @@ quoka_status paged_append(const quoka_paged_shape* shape, const void* k_new, con
  * The query of head h (KV head g = h / G) of sequence b, n = seq_len[b], attends to the
  * keys { j < n : j < n_sink or j >= n - window } (the new token's own key, if it is to be
  * seen, has been appended: position n - 1), out = softmax(q . k^T / sqrt(head_dim)) . v
- * with fp32 accumulation and softmax, stored in `dtype`.  n = 0 gives zeros; a row whose
+ * with fp32 accumulation and softmax, stored in `dtype` (bf16: the weights rounded as in
+ * window_chunk_attn; what the record gets is not).  No visible key gives zeros; a row whose
  * visible logits are all -infinity is 0 / 0, NaN (and so is what it adds to a record).
  * With a record, record[key] += sum over the G heads of the group of the key's softmax
  * weight, for every visible key of every (sequence, KV head); a page that several
@@ -459,12 +462,14 @@ quoka_status paged_decode_attn(const quoka_paged_shape* shape, const void* q, co
                                int max_len, int window, int n_sink, float* record, void* out,
                                void* workspace, size_t ws_bytes, void* stream);
 
-/* Bytes of device scratch paged_decode_attn() needs (0 if the arguments are invalid). */
+/* Bytes of device scratch paged_decode_attn() needs (0 if the arguments are invalid); they go by
+ * max_len, whatever the window. */
 size_t paged_decode_attn_workspace_size(const quoka_paged_shape* shape, int max_len, int with_record);
 
 /*
  * paged_evict - shrinks the cache of every sequence, each KV head by itself, to the rows
- * that received the most attention weight.
+ * that received the most attention weight (from paged_decode_attn with a record: right after a
+ * prompt was appended every record is 0, and ties keep the earliest rows).
  *
  * Of the n = seq_len[b] rows of (sequence b, KV head g), B = min(n, budget[b]) are kept:
  * the first min(n_sink, B); of what is left of B, up to n_recent of the latest; and of the

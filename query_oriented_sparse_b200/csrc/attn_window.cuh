@@ -6,12 +6,13 @@
 // fill it too.  One CTA walks the visible keys of a tile in blocks of 64: the first tokens, then
 // the window from the first row's oldest key to the last row's own, with the online softmax in
 // fp32; when the tiles are few, each tile's blocks are split over several CTAs, whose partials
-// window_join_kernel merges.  It is bound by the FMA units, so a thread holds 4 x 4
-// logits and 4 x D/16 outputs and reads shared memory in 16-byte vectors along the summed
-// axis (one read for eight FMAs; rows padded by 16 bytes, so that a quarter warp's reads hit
-// all banks), and the next block's rows come in by cp.async meanwhile: 29.8 TFLOP/s for 2048
-// queries through a window of 1024 keys at d 128, where scalar reads of single-buffered blocks
-// gave 20.9.  Blocks that some row does not see whole are masked by selection, and P.V skips
+// window_join_kernel merges.  It is bound by the FMAs and the shared-memory reads that feed
+// them: a thread holds 4 x 4 logits and 4 x D/16 outputs and reads in 16-byte vectors along the
+// summed axis (one read for eight FMAs; rows padded by 16 bytes, so that a quarter warp's reads
+// hit all banks), which keeps the shared-memory pipe busy for three quarters of the FMAs' time;
+// the next block's rows come in by cp.async meanwhile.  29.8 TFLOP/s, 40 % of the FMA rate, for
+// 2048 queries through a window of 1024 keys at d 128, where scalar reads of single-buffered
+// blocks gave 20.9.  Blocks that some row does not see whole are masked by selection, and P.V skips
 // masked keys there, so that a value that is not a number reaches only the rows that see it.
 #pragma once
 #include "attn_decode.cuh"

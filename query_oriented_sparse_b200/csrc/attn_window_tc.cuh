@@ -18,14 +18,15 @@
 // (columns 128 x and 128 x + 64, P over S), Q buffer and rings of four K and four V stages: one
 // tile's start, end and masked blocks pass under the other's work.  S of block j + 2 is issued
 // behind P.V of block j, so a softmax warp finds the next S done while its last block's products
-// run.  A block then takes about 850 clocks per SM.  Measured on 4096 queries of 32 heads, 8 KV
-// heads, window 4096, d 128: 257 us (1085 TFLOP/s; 265 without the
-// exponentials on the FMA pipe below).  One thread running the issuing loop, whose descriptors then
-// pass through general registers, costs 6 us more (70 clocks an MMA).
-// With blocks of 128 keys, which leave TMEM for one S per tile, so that each tile's products and
-// softmax wait for one another, 280; with one tile at a time whose blocks the two softmax groups
-// share, as in attn_tc2.cuh, 320.  8 sequences of 1024 queries, 16 heads to a KV head, window
-// 2047: 522 us against 616 with blocks of 128 keys.
+// run.  A block then takes about 880 clocks per SM.  Measured on 4096 queries of 32 heads, 8 KV
+// heads, window 4096, d 128: 257 us in a short run (1085 TFLOP/s; 265 without the exponentials on
+// the FMA pipe below) and 296 among other calls, where the power limit lowers the clock.  8
+// sequences of 1024 queries, 16 heads to a KV head, window 2047: 544 and 633 us.
+// Steps of the design, each against what it replaced: two tiles at once 306, one tile whose blocks
+// the two softmax groups share, as in attn_tc2.cuh, 320; blocks of 64 keys 266, blocks of 128, which
+// leave TMEM for one S per tile, so that each tile's products and softmax wait for one another, 280
+// (ragged 549, 616); a whole warp running the issuing loop 260, one thread, whose descriptors pass
+// through general registers (70 clocks an MMA), 266.
 // The clusters resident at once walk the tile list, cluster c taking tiles c, c + N, ...,
 // its two streams in turn; the last of an odd number both streams share by key blocks, and
 // stream 1's half reaches stream 0 through shared memory.
